@@ -237,6 +237,111 @@ KVP_API kvp_status kvp_score_static(const kvp_shape* shape, const uint16_t* q_wi
  * this device, read from the library's scratch array (synchronises `stream`). */
 KVP_API kvp_status kvp_score_static_status(void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The cache that a decode reads: pages of kept rows, appended to, attended over and kept at a
+ * budget while it grows.
+ *
+ * Every KV head of a sequence keeps its own rows (other positions, and under adaptive budgets
+ * another number of them), so pages belong to one KV head of one sequence:
+ *   k_pages, v_pages [num_pages, P, d]  a pool of pages of P rows, bf16 or fp16
+ *   table [b, hkv, M] int32             the pages of a head's rows: its row j lies in row j % P of
+ *                                       page table[j / P]. An entry outside [0, num_pages) is no
+ *                                       page: its rows are not there (never read or written; weight
+ *                                       zero in the attention and for the eviction).
+ *   lens  [b, hkv] int32                rows in use, taken as clamped to [0, M P]
+ *   acc   [num_pages, P] fp32           the attention weight each cached row has drawn so far
+ * No two live rows may share a place in the pool when a call writes to it. A cache with pages
+ * of all heads ([pages, hkv, P, d]) is this one with pages numbered page * hkv + head; a
+ * contiguous [b, hkv, B, d] (kvp_compact's output) is a pool of b hkv B / P pages when P
+ * divides B. Rows at or past a head's len are left as they were.
+ *
+ * These calls follow the conventions above. They have no device-side waits, and may be captured
+ * into a CUDA graph. Rows are addressed in 64 bits, so a pool may exceed 2^31 elements.
+ * ---------------------------------------------------------------------------------------- */
+typedef enum { KVP_BF16 = 0, KVP_FP16 = 1 } kvp_dtype;
+
+typedef struct {
+    int32_t batch;     /* b   >= 1 */
+    int32_t hq;        /* query heads, a multiple of hkv; G = hq / hkv <= 64 */
+    int32_t hkv;       /* KV heads >= 1; b * hkv <= 2^20 */
+    int32_t head_dim;  /* d: 64 or 128 */
+    int32_t page_size; /* P: 16, 32, 64, 128 or 256 rows */
+    int32_t num_pages; /* pages of the pool >= 1 */
+    int32_t max_pages; /* M >= 1: pages a head's table holds; M * P <= 2^23 */
+    int32_t dtype;     /* a kvp_dtype: of q, k, v, the pools and the attention's output */
+} kvp_cache_shape;
+
+/*
+ * Appends rows: row i of a head's new rows becomes its row lens + i. Fills a cache with the rows
+ * that kvp_compact or kvp_compact_ragged kept, and takes a decoded token's row (n = 1).
+ *   n       new rows per head, 0 <= n <= 2^23, when counts is NULL; else hkv * n rows per sequence,
+ *           head after head, counts[b, h] of them head h's (kvp_compact_ragged's layout; counts
+ *           below zero count as zero, and rows past hkv * n are not there); hkv * n < 2^31
+ *   k_new, v_new [b, hkv, n, d], or [b, hkv * n, d] with counts
+ *   weight  [b, hkv, n] or [b, hkv * n] fp32: the rows' first accumulated weights (the prefill's,
+ *           say); NULL: zero
+ *   acc     may be NULL (no weights are kept); weight is then NULL too
+ *   lens_out [b, hkv] int32 output, may be lens itself: lens + the rows appended, at most M P.
+ *           Rows past M P are dropped, and so are rows without a page (they still count).
+ */
+KVP_API kvp_status kvp_cache_append(const kvp_cache_shape* shape, const uint16_t* k_new,
+                                    const uint16_t* v_new, int32_t n, const int32_t* counts,
+                                    const float* weight, uint16_t* k_pages, uint16_t* v_pages, float* acc,
+                                    const int32_t* table, const int32_t* lens, int32_t* lens_out,
+                                    void* stream);
+
+/*
+ * Attention of one new token over the cache: for query head g of KV head h, over h's rows j,
+ *   t_gj = q_g . k_j / sqrt(d),  lse_g = log sum_j exp(t_gj),  p_gj = exp(t_gj - lse_g)
+ *   out_g = sum_j p_gj v_j,      acc_j += sum over the G query heads of h of p_gj
+ * A head without rows (or whose every t is -inf) gives out = 0, lse = -inf, and adds nothing.
+ *   q    [b, hq, d];  out [b, hq, d] output, may be q itself
+ *   lse  [b, hq] fp32 output, may be NULL
+ *   acc  updated in place, may be NULL
+ *   workspace  at least kvp_cache_attend_workspace_bytes(shape, acc != NULL) bytes
+ * Arithmetic: products of the inputs' type accumulated in fp32; logits, maximum, sums and joins
+ * in fp32. The weights that multiply v are rounded to the inputs' type: as a pair (value and
+ * remainder) when G <= 8. The cache is cut by its rows and the launch alone, and parts are joined
+ * in a fixed order: repeat calls agree bit for bit.
+ */
+KVP_API size_t kvp_cache_attend_workspace_bytes(const kvp_cache_shape* shape, int32_t accumulate);
+KVP_API kvp_status kvp_cache_attend(const kvp_cache_shape* shape, const uint16_t* q, const uint16_t* k_pages,
+                                    const uint16_t* v_pages, const int32_t* table, const int32_t* lens,
+                                    uint16_t* out, float* lse, float* acc, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+typedef struct {
+    int32_t budget;    /* B >= 1: rows a head may keep; B <= 2^23 */
+    int32_t sinks;     /* s >= 0: its first s rows always stay */
+    int32_t window;    /* w >= 0: and so do its last w; s + w <= B */
+} kvp_evict;
+
+/*
+ * Eviction by accumulated weight: a head with n = len rows over its budget t keeps its first s
+ * rows, its last w, and of the rows between the t - s - w that have drawn the most (acc; equal:
+ * lower row first; a weight that is negative or NaN counts as zero). A head at or under its
+ * budget stays as it is.
+ *   t = B, or budgets[b, h] clamped to [max(s + w, 1), B] where budgets is given
+ * The cache is compacted in place, moving no more rows than it must: kept rows below t - w stay
+ * where they are; the evicted places below t - w, ascending, take the kept rows that lie at or
+ * past t - w and before the window, ascending; the window's rows come last, in order, at
+ * [t - w, t). (Attention does not depend on the order of rows; which rows are the last w does.)
+ *   acc      input;  acc_out [num_pages, P] fp32 output: the kept rows' weights at their new
+ *            places, other entries untouched; may be acc itself
+ *   lens_out [b, hkv] int32 output, may be lens itself: min(n, t)
+ *   src      [b, hkv, B] int32 output, may be NULL: src[b, h, i] = the row that is now row i (-1
+ *            at and past lens_out), to carry along what else a program keeps per row
+ *   workspace  at least kvp_cache_evict_workspace_bytes(shape, evict) bytes
+ * A row that moves from or to a place without a page is not copied. Pages past
+ * ceil(lens_out / P) hold no rows any more and may be given to others.
+ */
+KVP_API size_t kvp_cache_evict_workspace_bytes(const kvp_cache_shape* shape, const kvp_evict* evict);
+KVP_API kvp_status kvp_cache_evict(const kvp_cache_shape* shape, const kvp_evict* evict,
+                                   const int32_t* budgets, uint16_t* k_pages, uint16_t* v_pages,
+                                   const float* acc, float* acc_out, const int32_t* table,
+                                   const int32_t* lens, int32_t* lens_out, int32_t* src,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 /* The name of the CUDA error behind the calling thread's most recent KVP_ERR_CUDA
  * ("cudaSuccess" if there was none). Host-only; never fails. */
 KVP_API const char* kvp_last_cuda_error(void);

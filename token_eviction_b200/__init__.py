@@ -16,9 +16,17 @@ The functions carry the C names:
 * ``kvp_compact_ragged(shape, k, v, idx, counts, k_out, v_out, stream=None)``
 * ``kvp_compact(shape, k, v, idx, k_out, v_out, stream=None)``
 * ``kvp_workspace_status(workspace, stream=None)``
+* ``kvp_cache_append(shape, k_new, v_new, k_pages, v_pages, table, lens, lens_out, acc=None, weight=None,
+  counts=None, stream=None)``
+* ``kvp_cache_attend(shape, q, k_pages, v_pages, table, lens, out, lse=None, acc=None, workspace=None,
+  stream=None)``
+* ``kvp_cache_evict(shape, evict, k_pages, v_pages, acc, acc_out, table, lens, lens_out, src=None,
+  budgets=None, workspace=None, stream=None)``
 * ``kvp_status_string(status)``
 
-plus ``evict_layer``, which allocates the outputs and runs all three calls.
+plus ``evict_layer``, which allocates the outputs and runs the first three calls, and
+``LayerCache``, the paged cache that a decode reads: it takes what ``evict_layer`` kept, appends
+and attends token by token, and keeps to a budget.
 
 There is no fallback: if ``libkvp.so`` is missing or cannot be loaded, importing this
 package raises.
@@ -63,6 +71,36 @@ def make_policy(sinks=0, pool_kernel=1, mode=RANK_PRODUCT) -> KvpPolicy:
     return KvpPolicy(int(sinks), int(pool_kernel), int(mode))
 
 
+class KvpCacheShape(ctypes.Structure):
+    """Mirror of ``kvp_cache_shape``: a paged cache and the query heads that read it."""
+    _fields_ = [("batch", ctypes.c_int32), ("hq", ctypes.c_int32), ("hkv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+    def __repr__(self):
+        return "KvpCacheShape(%s)" % ", ".join("%s=%d" % (n, getattr(self, n)) for n, _ in self._fields_)
+
+
+_DTYPES = (torch.bfloat16, torch.float16)     # by kvp_dtype
+
+
+def make_cache_shape(batch, hq, hkv, head_dim, page_size, num_pages, max_pages,
+                     dtype=torch.bfloat16) -> KvpCacheShape:
+    if dtype not in _DTYPES:
+        raise ValueError(f"a cache is torch.bfloat16 or torch.float16, got {dtype}")
+    return KvpCacheShape(int(batch), int(hq), int(hkv), int(head_dim), int(page_size), int(num_pages),
+                         int(max_pages), _DTYPES.index(dtype))
+
+
+class KvpEvict(ctypes.Structure):
+    """Mirror of ``kvp_evict``: rows a head keeps, the first and the last that always stay."""
+    _fields_ = [("budget", ctypes.c_int32), ("sinks", ctypes.c_int32), ("window", ctypes.c_int32)]
+
+
+def make_evict(budget, sinks=0, window=0) -> KvpEvict:
+    return KvpEvict(int(budget), int(sinks), int(window))
+
+
 class KvpError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -105,6 +143,17 @@ def _load():
     lib.kvp_workspace_status.restype = ctypes.c_int
     lib.kvp_score_static.argtypes = [S, P, P, P, P, P, P, P]
     lib.kvp_score_static.restype = ctypes.c_int
+    C, E = ctypes.POINTER(KvpCacheShape), ctypes.POINTER(KvpEvict)
+    lib.kvp_cache_append.argtypes = [C, P, P, ctypes.c_int32, P, P, P, P, P, P, P, P, P]
+    lib.kvp_cache_append.restype = ctypes.c_int
+    lib.kvp_cache_attend_workspace_bytes.argtypes = [C, ctypes.c_int32]
+    lib.kvp_cache_attend_workspace_bytes.restype = ctypes.c_size_t
+    lib.kvp_cache_attend.argtypes = [C, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.kvp_cache_attend.restype = ctypes.c_int
+    lib.kvp_cache_evict_workspace_bytes.argtypes = [C, E]
+    lib.kvp_cache_evict_workspace_bytes.restype = ctypes.c_size_t
+    lib.kvp_cache_evict.argtypes = [C, E, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.kvp_cache_evict.restype = ctypes.c_int
     lib.kvp_score_static_status.argtypes = [P]
     lib.kvp_score_static_status.restype = ctypes.c_int
     return lib
@@ -119,7 +168,8 @@ KERNELS_PER_LAYER = 3
 
 EXPORTED = ("kvp_workspace_bytes", "kvp_score", "kvp_select", "kvp_select_policy", "kvp_leverage",
             "kvp_adaptive_workspace_bytes", "kvp_select_adaptive", "kvp_compact_ragged", "kvp_compact",
-            "kvp_workspace_status",
+            "kvp_workspace_status", "kvp_cache_append", "kvp_cache_attend_workspace_bytes", "kvp_cache_attend",
+            "kvp_cache_evict_workspace_bytes", "kvp_cache_evict",
             "kvp_score_static", "kvp_score_static_status", "kvp_status_string", "kvp_last_cuda_error")
 
 
@@ -333,3 +383,200 @@ def evict_layer(q_win, k, v, window: int, budget: int, buffers: LayerBuffers | N
     kvp_select(sh, buffers.score, buffers.idx, buffers.workspace, stream)
     kvp_compact(sh, k, v, buffers.idx, buffers.k_out, buffers.v_out, stream)
     return buffers
+
+
+# ---- the paged cache
+
+
+def _cache_args(items):
+    """Pointers of `items`, (tensor or None, name, dtype, shape) each: CUDA tensors on one device,
+    contiguous, of that type and shape. Returns the pointers and the device's index."""
+    ptrs, dev = [], None
+    for t, name, dtype, shape in items:
+        if t is None:
+            ptrs.append(None)
+            continue
+        ptrs.append(_ptr(t, name, dtype, shape))
+        if dev is None:
+            dev = t.device.index
+        elif t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{dev}")
+    return ptrs, dev
+
+
+def _on(dev, call, *args, stream=None):
+    """call(*args, stream) with the tensors' device current, on `stream` (by default that device's
+    current one): streams and launches belong to a device."""
+    if dev == torch.cuda.current_device():
+        return call(*args, _stream(stream))
+    with torch.cuda.device(dev):
+        return call(*args, _stream(stream))
+
+
+def _kept_for(stream, workspace):
+    """A workspace that the call made itself lives until `stream` is done with it."""
+    if stream is not None:
+        workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                else torch.cuda.ExternalStream(int(stream), device=workspace.device))
+
+
+def _cache_workspace(nbytes, what, device):
+    if nbytes == 0:
+        raise KvpError(2, what)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def attend_workspace_for(shape, accumulate=False, device=None) -> torch.Tensor:
+    n = int(_lib.kvp_cache_attend_workspace_bytes(ctypes.byref(shape), int(bool(accumulate))))
+    return _cache_workspace(n, "kvp_cache_attend_workspace_bytes", device)
+
+
+def evict_workspace_for(shape, evict, device=None) -> torch.Tensor:
+    n = int(_lib.kvp_cache_evict_workspace_bytes(ctypes.byref(shape), ctypes.byref(evict)))
+    return _cache_workspace(n, "kvp_cache_evict_workspace_bytes", device)
+
+
+def _pool(sh, k_pages, v_pages, table, lens, dt):
+    pool, heads = (sh.num_pages, sh.page_size, sh.head_dim), (sh.batch, sh.hkv)
+    return [(k_pages, "k_pages", dt, pool), (v_pages, "v_pages", dt, pool),
+            (table, "table", torch.int32, heads + (sh.max_pages,)), (lens, "lens", torch.int32, heads)]
+
+
+def _dtype(sh):
+    if not 0 <= sh.dtype < len(_DTYPES):
+        raise KvpError(2, "kvp_cache_shape")
+    return _DTYPES[sh.dtype]
+
+
+def _required(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is required")
+
+
+def kvp_cache_append(shape, k_new, v_new, k_pages, v_pages, table, lens, lens_out, acc=None, weight=None,
+                     counts=None, stream=None):
+    """Appends n rows per head: k_new and v_new [b, hkv, n, d], or packed head after head
+    [b, hkv * n, d] with counts [b, hkv]. weight: the rows' first accumulated weights, shaped
+    like k_new without its last dimension. lens_out may be lens."""
+    sh = shape
+    _required(k_new=k_new, v_new=v_new, k_pages=k_pages, v_pages=v_pages, table=table, lens=lens,
+              lens_out=lens_out)
+    dt, b, hkv = _dtype(sh), sh.batch, sh.hkv
+    if counts is None:
+        n = k_new.shape[2] if k_new.dim() == 4 else -1
+        rows = (b, hkv, n)
+    else:
+        n = k_new.shape[1] // hkv if k_new.dim() == 3 else -1
+        rows = (b, hkv * n)
+    if n < 0:
+        raise ValueError("k_new must be [b, hkv, n, d], or [b, hkv * n, d] with counts")
+    (k, v, kp, vp, pt, pl, plo, pa, pw, pc), dev = _cache_args(
+        [(k_new, "k_new", dt, rows + (sh.head_dim,)), (v_new, "v_new", dt, rows + (sh.head_dim,))]
+        + _pool(sh, k_pages, v_pages, table, lens, dt)
+        + [(lens_out, "lens_out", torch.int32, (b, hkv)),
+           (acc, "acc", torch.float32, (sh.num_pages, sh.page_size)),
+           (weight, "weight", torch.float32, rows), (counts, "counts", torch.int32, (b, hkv))])
+    st = _on(dev, _lib.kvp_cache_append, ctypes.byref(sh), k, v, n, pc, pw, kp, vp, pa, pt, pl, plo,
+             stream=stream)
+    if st != KVP_OK:
+        raise KvpError(st, "kvp_cache_append")
+
+
+def kvp_cache_attend(shape, q, k_pages, v_pages, table, lens, out, lse=None, acc=None, workspace=None,
+                     stream=None):
+    """Attention of one token q [b, hq, d] over the cache; acc gains each row's weights."""
+    sh = shape
+    _required(q=q, k_pages=k_pages, v_pages=v_pages, table=table, lens=lens, out=out)
+    dt, heads = _dtype(sh), (sh.batch, sh.hq)
+    own = workspace is None
+    if own:
+        workspace = attend_workspace_for(sh, acc is not None, q.device)
+    (kp, vp, pt, pl, pq, po, ps, pa, pw), dev = _cache_args(
+        _pool(sh, k_pages, v_pages, table, lens, dt)
+        + [(q, "q", dt, heads + (sh.head_dim,)), (out, "out", dt, heads + (sh.head_dim,)),
+           (lse, "lse", torch.float32, heads), (acc, "acc", torch.float32, (sh.num_pages, sh.page_size)),
+           (workspace, "workspace", torch.uint8, None)])
+    st = _on(dev, _lib.kvp_cache_attend, ctypes.byref(sh), pq, kp, vp, pt, pl, po, ps, pa, pw,
+             workspace.numel(), stream=stream)
+    if own:
+        _kept_for(stream, workspace)
+    if st != KVP_OK:
+        raise KvpError(st, "kvp_cache_attend")
+
+
+def kvp_cache_evict(shape, evict, k_pages, v_pages, acc, acc_out, table, lens, lens_out, src=None,
+                    budgets=None, workspace=None, stream=None):
+    """Each head keeps its first `sinks` rows, its last `window` and the heaviest between them, up to
+    its budget (a KvpEvict, or a dict of make_evict's arguments). In place; acc_out may be acc
+    and lens_out lens."""
+    sh = shape
+    ev = evict if isinstance(evict, KvpEvict) else make_evict(**evict)
+    _required(k_pages=k_pages, v_pages=v_pages, acc=acc, acc_out=acc_out, table=table, lens=lens,
+              lens_out=lens_out)
+    dt, heads, pool = _dtype(sh), (sh.batch, sh.hkv), (sh.num_pages, sh.page_size)
+    own = workspace is None
+    if own:
+        workspace = evict_workspace_for(sh, ev, acc.device)
+    (kp, vp, pt, pl, pa, pao, plo, ps, pb, pw), dev = _cache_args(
+        _pool(sh, k_pages, v_pages, table, lens, dt)
+        + [(acc, "acc", torch.float32, pool), (acc_out, "acc_out", torch.float32, pool),
+           (lens_out, "lens_out", torch.int32, heads), (src, "src", torch.int32, heads + (ev.budget,)),
+           (budgets, "budgets", torch.int32, heads), (workspace, "workspace", torch.uint8, None)])
+    st = _on(dev, _lib.kvp_cache_evict, ctypes.byref(sh), ctypes.byref(ev), pb, kp, vp, pa, pao, pt, pl, plo,
+             ps, pw, workspace.numel(), stream=stream)
+    if own:
+        _kept_for(stream, workspace)
+    if st != KVP_OK:
+        raise KvpError(st, "kvp_cache_evict")
+
+
+class LayerCache:
+    """One layer's paged cache through a decode: filled with the rows an eviction kept, then a token at
+    a time appended, attended over and, where a budget is given, evicted by accumulated weight.
+
+    Holds up to `capacity` rows per KV head, in pages of its own (table and pools may be replaced by
+    a program that shares a pool between layers or requests). `evict`: a KvpEvict; heads over its
+    budget are cut back in every step.
+    """
+
+    def __init__(self, batch, hq, hkv, head_dim, capacity, page_size=64, evict: KvpEvict | None = None,
+                 dtype=torch.bfloat16, device="cuda"):
+        width = -(-capacity // page_size)
+        self.shape = make_cache_shape(batch, hq, hkv, head_dim, page_size, batch * hkv * width, width, dtype)
+        self.evict_policy = evict
+        new = lambda shape, dt: torch.zeros(shape, dtype=dt, device=device)
+        self.k_pages = new((self.shape.num_pages, page_size, head_dim), dtype)
+        self.v_pages = torch.zeros_like(self.k_pages)
+        self.table = torch.arange(self.shape.num_pages, dtype=torch.int32, device=device).view(batch, hkv, width)
+        self.lens = new((batch, hkv), torch.int32)
+        self.acc = new((self.shape.num_pages, page_size), torch.float32) if evict is not None else None
+        self.out = new((batch, hq, head_dim), dtype)
+        self.lse = new((batch, hq), torch.float32)
+        self.workspace = attend_workspace_for(self.shape, evict is not None, device)
+        self.evict_workspace = evict_workspace_for(self.shape, evict, device) if evict is not None else None
+
+    def append(self, k_new, v_new, weight=None, counts=None, stream=None):
+        """Rows behind those that each head holds: [b, hkv, n, d], or [b, hkv * n, d] with counts."""
+        kvp_cache_append(self.shape, k_new, v_new, self.k_pages, self.v_pages, self.table, self.lens,
+                         self.lens, self.acc, weight, counts, stream)
+
+    def attend(self, q, stream=None) -> torch.Tensor:
+        """Attention of q [b, hq, d] over the rows held; returns self.out (self.lse beside it)."""
+        kvp_cache_attend(self.shape, q, self.k_pages, self.v_pages, self.table, self.lens, self.out,
+                         self.lse, self.acc, self.workspace, stream)
+        return self.out
+
+    def evict(self, stream=None):
+        """Cuts every head that is over the budget back to it."""
+        kvp_cache_evict(self.shape, self.evict_policy, self.k_pages, self.v_pages, self.acc, self.acc,
+                        self.table, self.lens, self.lens, None, None, self.evict_workspace, stream)
+
+    def step(self, q, k_new, v_new, stream=None) -> torch.Tensor:
+        """One decoded token: its key and value [b, hkv, 1, d] join the cache, q attends, and the cache is
+        cut back to its budget."""
+        self.append(k_new, v_new, stream=stream)
+        out = self.attend(q, stream)
+        if self.evict_policy is not None:
+            self.evict(stream)
+        return out

@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "kvp.h"
+#include "kvp_cache.cuh"
 #include "kvp_internal.cuh"
 
 namespace kvp {
@@ -204,6 +205,80 @@ extern "C" kvp_status kvp_compact(const kvp_shape* shape, const uint16_t* k, con
     return KVP_OK;
 }
 
+// ---- the paged cache
+
+extern "C" kvp_status kvp_cache_append(const kvp_cache_shape* shape, const uint16_t* k_new,
+                                       const uint16_t* v_new, int32_t n, const int32_t* counts,
+                                       const float* weight, uint16_t* k_pages, uint16_t* v_pages, float* acc,
+                                       const int32_t* table, const int32_t* lens, int32_t* lens_out,
+                                       void* stream) {
+    if (!shape || !k_pages || !v_pages || !table || !lens || !lens_out) return KVP_ERR_NULL;
+    if (n != 0 && (!k_new || !v_new)) return KVP_ERR_NULL;
+    if (!cache_shape_ok(*shape) || n < 0 || n > kMaxCacheRows || (weight && !acc)) return KVP_ERR_SHAPE;
+    if ((long long)shape->hkv * n > INT32_MAX) return KVP_ERR_SHAPE;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(counts) || !aligned16(weight) ||
+        !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(acc) || !aligned16(table) ||
+        !aligned16(lens) || !aligned16(lens_out))
+        return KVP_ERR_ALIGN;
+    const cudaError_t e = launch_append(*shape, k_new, v_new, n, counts, weight, k_pages, v_pages, acc, table,
+                                        lens, lens_out, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_failed(e);
+    return KVP_OK;
+}
+
+extern "C" size_t kvp_cache_attend_workspace_bytes(const kvp_cache_shape* shape, int32_t accumulate) {
+    if (!shape || !cache_shape_ok(*shape)) return 0;
+    return attend_workspace_bytes(*shape, accumulate != 0);
+}
+
+extern "C" kvp_status kvp_cache_attend(const kvp_cache_shape* shape, const uint16_t* q, const uint16_t* k_pages,
+                                       const uint16_t* v_pages, const int32_t* table, const int32_t* lens,
+                                       uint16_t* out, float* lse, float* acc, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    if (!shape || !q || !k_pages || !v_pages || !table || !lens || !out) return KVP_ERR_NULL;
+    const size_t need = kvp_cache_attend_workspace_bytes(shape, acc != nullptr);
+    if (need == 0) return KVP_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(table) || !aligned16(lens) ||
+        !aligned16(out) || !aligned16(lse) || !aligned16(acc))
+        return KVP_ERR_ALIGN;
+    if (!workspace || workspace_bytes < need) return KVP_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return KVP_ERR_ALIGN;
+    const cudaError_t e = launch_attend(*shape, q, k_pages, v_pages, table, lens, out, lse, acc, workspace,
+                                        (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_failed(e);
+    return KVP_OK;
+}
+
+static bool evict_ok(const kvp_evict& e) {
+    return e.sinks >= 0 && e.window >= 0 && e.budget >= 1 && e.budget <= kMaxCacheRows &&
+           (long long)e.sinks + e.window <= e.budget;
+}
+
+extern "C" size_t kvp_cache_evict_workspace_bytes(const kvp_cache_shape* shape, const kvp_evict* evict) {
+    if (!shape || !evict || !cache_shape_ok(*shape) || !evict_ok(*evict)) return 0;
+    return evict_workspace_bytes(*shape, *evict);
+}
+
+extern "C" kvp_status kvp_cache_evict(const kvp_cache_shape* shape, const kvp_evict* evict,
+                                      const int32_t* budgets, uint16_t* k_pages, uint16_t* v_pages,
+                                      const float* acc, float* acc_out, const int32_t* table,
+                                      const int32_t* lens, int32_t* lens_out, int32_t* src, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+    if (!shape || !evict || !k_pages || !v_pages || !acc || !acc_out || !table || !lens || !lens_out)
+        return KVP_ERR_NULL;
+    const size_t need = kvp_cache_evict_workspace_bytes(shape, evict);
+    if (need == 0) return KVP_ERR_SHAPE;
+    if (!aligned16(budgets) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(acc) ||
+        !aligned16(acc_out) || !aligned16(table) || !aligned16(lens) || !aligned16(lens_out) || !aligned16(src))
+        return KVP_ERR_ALIGN;
+    if (!workspace || workspace_bytes < need) return KVP_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return KVP_ERR_ALIGN;
+    const cudaError_t e = launch_evict(*shape, *evict, budgets, k_pages, v_pages, acc, acc_out, table, lens,
+                                       lens_out, src, workspace, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_failed(e);
+    return KVP_OK;
+}
+
 extern "C" kvp_status kvp_workspace_status(const void* workspace, void* stream) {
     if (!workspace) return KVP_ERR_NULL;
     if (!aligned16(workspace)) return KVP_ERR_ALIGN;
@@ -219,15 +294,17 @@ extern "C" KVP_API void kvp_debug_set_fault(int extra_peers, unsigned long long 
 
 // Debug builds only: copy out (and clear) the first failed device-side bounds check.
 extern "C" KVP_API int kvp_debug_take_check_unit(int unit, int* out4) {
-    int (*readers[5])(int*) = {take_check_score, take_check_select, take_check_compact,
-                               take_check_leverage, take_check_adaptive};
-    if (unit < 0 || unit > 4) return -1;
+    int (*readers[8])(int*) = {take_check_score, take_check_select, take_check_compact,
+                               take_check_leverage, take_check_adaptive, take_check_append,
+                               take_check_attend, take_check_evict};
+    if (unit < 0 || unit > 7) return -1;
     return readers[unit](out4);
 }
 
 extern "C" KVP_API int kvp_debug_take_check(int* out4) {
-    int (*readers[5])(int*) = {take_check_score, take_check_select, take_check_compact,
-                               take_check_leverage, take_check_adaptive};
+    int (*readers[8])(int*) = {take_check_score, take_check_select, take_check_compact,
+                               take_check_leverage, take_check_adaptive, take_check_append,
+                               take_check_attend, take_check_evict};
     out4[0] = out4[1] = out4[2] = out4[3] = 0;
     for (auto rd : readers) {
         int v[4];

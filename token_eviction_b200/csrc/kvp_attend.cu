@@ -1,0 +1,717 @@
+// Attention of one new token over a paged cache, split over the cache's rows and joined:
+//   t_gj = q_g . k_j / sqrt(d), out_g = sum_j 2^(t_gj log2 e - lse2_g) v_j, acc_j += sum_g p_gj.
+//
+// Bound: every cached row is read once, 4 d bytes of key and value for 4 G d flops: G flops a
+// byte, far below what the card can multiply while it reads (G <= 16 needs under 110 TFLOP/s at
+// the measured 6.56 TB/s). So the matrix products are warp-level mma.sync m16n8k16, whose
+// operands go from the ring in shared memory to registers with no barrier between warps, and
+// the kernel is built around bytes in flight.
+//
+// attend_split: the units (a head's rows against up to 8, or 16, of its query heads) laid end to
+// end are one run of tiles of 64 rows, cut evenly over two CTAs per SM, whatever the lengths.
+// Each of a CTA's four warps streams its 16 rows of every tile through a ring of its own
+// (cp.async, 16-byte pieces, swizzled for ldmatrix), keeps the running maximum and sum of a
+// softmax, and never waits for another warp until the unit ends. There the four warps' parts
+// are joined in shared memory; a unit that lies within one CTA is finished, others leave a part
+// (unnormalised output, maximum, sum) in the workspace.
+// attend_join: joins the parts of the units that were cut, in the order of the rows, and adds
+// the attention weights to acc, from the logits that attend_split left in the workspace (4 G
+// bytes a row against 4 d of the row itself, most of them still in L2).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "kvp_cache.cuh"
+#include "kvp_ptx.cuh"
+
+namespace kvp {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kGroup = 16;                        // rows a warp takes at a time
+constexpr int kTile = kWarps * kGroup;            // rows a CTA takes at a time
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxGrid = kPlanGrid * kCtasPerSm;  // the workspace holds parts for as many CTAs
+constexpr int kJoinThreads = 256;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -3.4028234663852886e38f;  // of a maximum over nothing: finite, so that
+                                                    // differences of maxima are never inf - inf
+
+// Where a CTA's run begins: its unit, the tile within it.
+struct Start {
+    int unit, tile;
+};
+
+struct AttendArgs {
+    CacheView c;
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    uint16_t* out;
+    float* lse;          // NULL: not wanted
+    float* acc;          // NULL: not wanted
+    int G, ng, gq;       // query heads per head; units per head; query heads per unit (the last: fewer)
+    float scale2;        // log2 e / sqrt(d)
+    // workspace
+    Start* starts;       // [grid]
+    long long* total;    // tiles
+    uint32_t* first;     // [units]: the unit's first tile
+    float2* stats;       // [2 grid][gq]: a part's maximum and sum, log2 domain
+    float* parts;        // [2 grid][gq][d]: a part's unnormalised output
+    float* lse2;         // [heads * G]: of units that were not cut
+    float* logits;       // [heads * G][cap], log2 domain; NULL without acc
+};
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// T tiles cut over the first `parties` CTAs, none of them without a tile: CTA c takes
+// [cut(c), cut(c + 1)).
+__device__ __forceinline__ int parties_of(long long T, int grid) { return (int)min(T, (long long)grid); }
+__device__ __forceinline__ long long cut(long long c, long long T, int parties) { return c * T / parties; }
+__device__ __forceinline__ int cutter_of(long long t, long long T, int parties) {   // the CTA that takes tile t
+    return (int)(((t + 1) * parties + T - 1) / T - 1);
+}
+
+// ---- types
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+    static constexpr float kBias = 0.f;      // added to a weight's exponent before rounding
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t p) {
+        return make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    }
+};
+template <>
+struct Pair<__half> {
+    // Weights lie in [0, 1] and fp16 has no normal number below 2^-14: they are kept 2^14
+    // larger (so is their sum), which puts full precision down to 2^-28 of the largest.
+    static constexpr float kBias = 14.f;
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t p) {
+        return __half22float2(*reinterpret_cast<__half2*>(&p));
+    }
+    static __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    }
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr)
+                 : "memory");
+}
+// 16 bytes global -> shared, or 16 zero bytes when `bytes` is 0.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Where tile `want` of the run lies: every thread of the CTA sums a stretch of heads' tiles, and
+// the one whose stretch holds `want` walks it. Sets *at (shared) and returns the total.
+__device__ __forceinline__ long long find_start(const CacheView& c, int ng, int grid, int cta,
+                                                long long* warp_sums, Start* at) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (c.heads + kThreads - 1) / kThreads;
+    const int h0 = min(c.heads, tid * per), h1 = min(c.heads, h0 + per);
+    long long sum = 0;
+    for (int h = h0; h < h1; ++h) sum += (long long)tiles_of(c.len(h)) * ng;
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    long long before = 0, T = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += warp_sums[w];
+        T += warp_sums[w];
+    }
+    const int parties = parties_of(T, grid);
+    long long from = before + inc - sum;
+    const long long want = cta < parties ? cut(cta, T, parties) : -1;
+    if (want >= from && want < from + sum) {
+        for (int h = h0; h < h1; ++h) {
+            const int nt = tiles_of(c.len(h));
+            const long long n = (long long)nt * ng;
+            if (want < from + n) {
+                const int i = (int)(want - from);
+                at->unit = h * ng + i / nt;
+                at->tile = i % nt;
+                break;
+            }
+            from += n;
+        }
+    }
+    __syncthreads();
+    return T;
+}
+
+// A warp's walk over the units that have tiles, from a given one on. A register of each lane
+// holds one of 32 heads' lengths, so that a stretch of empty heads costs one load for 32.
+struct Walk {
+    int head, sub, tile, nt, len;   // unit = head * ng + sub
+    int base, lane_len;
+
+    __device__ __forceinline__ void load(const CacheView& c) {
+        const int h = base + (threadIdx.x & 31);
+        lane_len = h < c.heads ? c.len(h) : 0;
+    }
+    __device__ __forceinline__ void begin(const CacheView& c, int ng, const Start& s) {
+        head = s.unit / ng;
+        sub = s.unit - head * ng;
+        tile = s.tile;
+        base = head & ~31;
+        load(c);
+        len = __shfl_sync(0xffffffffu, lane_len, head & 31);
+        nt = tiles_of(len);
+    }
+    // The next tile; the caller knows that there is one.
+    __device__ __forceinline__ void next(const CacheView& c, int ng) {
+        if (++tile < nt) return;
+        tile = 0;
+        if (++sub < ng) return;
+        sub = 0;
+        ++head;
+        while (head < c.heads) {
+            if ((head & ~31) != base) {
+                base = head & ~31;
+                load(c);
+            }
+            const unsigned live = __ballot_sync(0xffffffffu, lane_len > 0) >> (head & 31);
+            if (live) {
+                head += __ffs(live) - 1;
+                break;
+            }
+            head = base + 32;
+        }
+        len = __shfl_sync(0xffffffffu, lane_len, head & 31);
+        nt = tiles_of(len);
+    }
+};
+
+// What a warp notes about a group when it issues its loads and reads when it consumes it.
+struct Meta {
+    int unit, row0;      // the group's first row within the head
+    int valid;           // rows of it that are there (0: nothing was loaded)
+    int flags;           // kFirst, kLast: of the unit, within this CTA's run; kWhole: the run has all of the unit
+};
+constexpr int kFirst = 1, kLast = 2, kWhole = 4;
+
+// Elements: T. D: head dimension. kWide: up to 16 query heads a unit, one row each of the MMA's
+// 16; else up to 8, whose weights fill rows 0-7 and the remainders left by rounding them to T
+// rows 8-15: the product with V then carries about twice T's precision, for free, since the
+// MMA has 16 rows anyway.
+template <typename T, int D, bool kWide, int kStages>
+struct Split {
+    static constexpr int kRowBytes = D * 2;
+    static constexpr int kChunks = D / 8;                       // 16-byte chunks of a row
+    static constexpr int kHalf = kGroup * kRowBytes;            // a group's keys (then its values)
+    static constexpr int kStage = 2 * kHalf;
+    static constexpr int kQ = kWide ? 16 : 8;                   // query heads a unit
+    static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage;
+    static_assert(kQ * D * 4 <= kStage, "a warp's part is joined in the stage it has consumed");
+};
+
+template <typename T, int D, bool kWide, int kStages>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const AttendArgs a) {
+    using S = Split<T, D, kWide, kStages>;
+    constexpr int kRowBytes = S::kRowBytes, kQ = S::kQ;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ long long warp_sums[kWarps];
+    __shared__ Start at;
+    __shared__ Meta meta[kWarps][kStages];
+    __shared__ float2 sh_stat[kWarps][kQ];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int gid = lane >> 2, tig = lane & 3;
+    const int grid = gridDim.x, cta = blockIdx.x;
+
+    ptx::grid_dependency_wait();
+    const long long T_ = find_start(a.c, a.ng, grid, cta, warp_sums, &at);
+    const int parties = parties_of(T_, grid);
+    if (tid == 0 && cta == 0) *a.total = T_;
+    if (cta >= parties) return;
+    const long long r0 = cut(cta, T_, parties);
+    const int steps = (int)(cut(cta + 1, T_, parties) - r0);
+    if (tid == 0) a.starts[cta] = at;
+
+    // ---- the issuing side: one group ahead of its loads, so that its page is at hand
+    Walk w;
+    w.begin(a.c, a.ng, at);
+    const uint32_t my_ring = ptx::smem_u32(ring) + warp * kStages * S::kStage;
+    auto page_of = [&]() -> int {            // of the walk's current group; -1: nothing to load
+        const int row0 = w.tile * kTile + warp * kGroup;
+        if (row0 >= w.len) return -1;
+        const int p = a.c.table[(size_t)w.head * a.c.max_pages + (row0 >> a.c.page_shift)];
+        return p < 0 || p >= a.c.num_pages ? -1 : p;
+    };
+    int issued = 0, page = page_of();
+    bool fresh = true;                       // the walk's tile is the run's first of its unit
+    bool begins = w.tile == 0;               // and the unit's first
+    // lanes of a load: kChunks lanes to a row, so 32 / kChunks rows at a time
+    constexpr int kRowsAt = 32 / S::kChunks;
+    const int chunk = lane % S::kChunks, lrow = lane / S::kChunks;
+    auto issue = [&]() {
+        if (issued < steps) {
+            const int stage = issued % kStages;
+            const int row0 = w.tile * kTile + warp * kGroup;
+            const int valid = page < 0 ? 0 : min(kGroup, w.len - row0);
+            const bool last = w.tile == w.nt - 1 || issued == steps - 1;
+            if (lane == 0) {
+                Meta m;
+                m.unit = w.head * a.ng + w.sub;
+                m.row0 = row0;
+                m.valid = valid;
+                m.flags = (fresh ? kFirst : 0) | (last ? kLast : 0) |
+                          (last && begins && w.tile == w.nt - 1 ? kWhole : 0);
+                meta[warp][stage] = m;
+                // the unit's place in the run, for the join
+                if (warp == 0 && w.tile == 0) a.first[m.unit] = (uint32_t)(r0 + issued);
+            }
+            if (valid > 0) {
+                const size_t row = ((size_t)page << a.c.page_shift) + (row0 & ((1 << a.c.page_shift) - 1));
+                const uint8_t* ks = (const uint8_t*)a.k + (row + lrow) * kRowBytes + chunk * 16;
+                const uint8_t* vs = (const uint8_t*)a.v + (row + lrow) * kRowBytes + chunk * 16;
+                const uint32_t dst = my_ring + stage * S::kStage + lrow * kRowBytes;
+#pragma unroll
+                for (int i = 0; i < kGroup / kRowsAt; ++i) {
+                    const int r = i * kRowsAt;
+                    // chunk ^ (row & 7), row = lrow + r: lrow < kRowsAt and r a multiple of kRowsAt
+                    const uint32_t off = r * kRowBytes + ((chunk ^ (lrow & 7) ^ (r & 7)) << 4);
+                    const bool in = lrow + r < valid;
+                    const size_t step = in ? (size_t)r * kRowBytes : 0;
+                    cp16(dst + off, in ? ks + step : (const uint8_t*)a.k, in ? 16 : 0);
+                    cp16(dst + off + S::kHalf, in ? vs + step : (const uint8_t*)a.v, in ? 16 : 0);
+                }
+            }
+            ++issued;
+            if (issued < steps) {
+                const int u = w.head * a.ng + w.sub;
+                w.next(a.c, a.ng);
+                fresh = w.head * a.ng + w.sub != u;
+                if (fresh) begins = true;
+                page = page_of();
+            }
+        }
+        cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue();
+
+    // ---- the consuming side
+    constexpr int kNt = D / 8;                // 8-column tiles of the output
+    float o[kNt][4];
+    float m_run[2], l_run[2];                 // of rows gid and gid + 8 (the latter: kWide only)
+    uint32_t qf[D / 16][kWide ? 4 : 2];
+    const int b_row = (lane & 7) + ((lane >> 4) & 1) * 8, b_chunk = (lane >> 3) & 1;   // keys
+    const int v_row = (lane & 7) + ((lane >> 3) & 1) * 8, v_chunk = (lane >> 4) & 1;   // values
+    int segment = 0;
+
+    for (int step = 0; step < steps; ++step) {
+        const int stage = step % kStages;
+        cp_wait<kStages - 2>();
+        __syncwarp();
+        const Meta m = meta[warp][stage];
+        issue();                              // into the stage consumed one step ago
+        const uint32_t sk = my_ring + stage * S::kStage, sv = sk + S::kHalf;
+        const int head = m.unit / a.ng, g0 = (m.unit - head * a.ng) * a.gq;
+        const int nq = min(a.gq, a.G - g0);   // query heads of this unit
+        if (m.flags & kFirst) {
+#pragma unroll
+            for (int i = 0; i < kNt; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+            m_run[0] = m_run[1] = kLowest;
+            l_run[0] = l_run[1] = 0.f;
+            const uint32_t* qp = (const uint32_t*)(a.q + ((size_t)head * a.G + g0) * D);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const int at32 = ks * 8 + tig;          // pairs of columns
+                qf[ks][0] = gid < nq ? qp[gid * (D / 2) + at32] : 0u;
+                qf[ks][1] = gid < nq ? qp[gid * (D / 2) + at32 + 4] : 0u;
+                if (kWide) {
+                    qf[ks][2] = gid + 8 < nq ? qp[(gid + 8) * (D / 2) + at32] : 0u;
+                    qf[ks][3] = gid + 8 < nq ? qp[(gid + 8) * (D / 2) + at32 + 4] : 0u;
+                }
+            }
+        }
+        if (m.valid > 0) {
+            // logits of 16 rows: two tiles of 8 rows, two chains each
+            float c[2][2][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                uint32_t b0, b1, b2, b3;
+                ldsm4(sk + b_row * kRowBytes + (((2 * ks + b_chunk) ^ (b_row & 7)) << 4), b0, b1, b2, b3);
+                const uint32_t a1 = kWide ? qf[ks][kWide ? 2 : 0] : 0u, a3 = kWide ? qf[ks][kWide ? 3 : 0] : 0u;
+                Pair<T>::mma(c[ks & 1][0], qf[ks][0], a1, qf[ks][1], a3, b0, b1);
+                Pair<T>::mma(c[ks & 1][1], qf[ks][0], a1, qf[ks][1], a3, b2, b3);
+            }
+            float t[2][4];                    // [8-row tile][row gid: 2 cached rows, row gid + 8: 2]
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = n * 8 + 2 * tig + (i & 1);
+                    t[n][i] = j < m.valid ? (c[0][n][i] + c[1][n][i]) * a.scale2 : -INFINITY;
+                }
+            if (a.logits) {
+                float* lp = a.logits + ((size_t)head * a.G + g0) * a.c.cap() + m.row0 + 2 * tig;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    if (gid < nq) *(float2*)(lp + (size_t)gid * a.c.cap() + n * 8) = make_float2(t[n][0], t[n][1]);
+                    if (kWide && gid + 8 < nq)
+                        *(float2*)(lp + (size_t)(gid + 8) * a.c.cap() + n * 8) = make_float2(t[n][2], t[n][3]);
+                }
+            }
+            uint32_t pa[4];                   // the weights as the A operand of P V
+#pragma unroll
+            for (int r = 0; r < (kWide ? 2 : 1); ++r) {
+                float mx = fmaxf(fmaxf(t[0][2 * r], t[0][2 * r + 1]), fmaxf(t[1][2 * r], t[1][2 * r + 1]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float m_new = fmaxf(m_run[r], mx);
+                if (__any_sync(0xffffffffu, m_new > m_run[r])) {
+                    const float f = ptx::ex2(m_run[r] - m_new);
+                    l_run[r] *= f;
+#pragma unroll
+                    for (int i = 0; i < kNt; ++i) {
+                        o[i][2 * r] *= f;
+                        o[i][2 * r + 1] *= f;
+                        if (!kWide) {         // rows 8-15 are the same query heads' remainders
+                            o[i][2] *= f;
+                            o[i][3] *= f;
+                        }
+                    }
+                    m_run[r] = m_new;
+                }
+                const float off = Pair<T>::kBias - m_run[r];
+                const float p0 = ptx::ex2(t[0][2 * r] + off), p1 = ptx::ex2(t[0][2 * r + 1] + off);
+                const float p2 = ptx::ex2(t[1][2 * r] + off), p3 = ptx::ex2(t[1][2 * r + 1] + off);
+                l_run[r] += (p0 + p1) + (p2 + p3);
+                pa[r] = Pair<T>::pack(p0, p1);
+                pa[r + 2] = Pair<T>::pack(p2, p3);
+                if (!kWide) {
+                    const float2 h0 = Pair<T>::unpack(pa[0]), h1 = Pair<T>::unpack(pa[2]);
+                    pa[1] = Pair<T>::pack(p0 - h0.x, p1 - h0.y);
+                    pa[3] = Pair<T>::pack(p2 - h1.x, p3 - h1.y);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kNt; i += 2) {
+                uint32_t b0, b1, b2, b3;
+                ldsm4t(sv + v_row * kRowBytes + (((i + v_chunk) ^ (v_row & 7)) << 4), b0, b1, b2, b3);
+                Pair<T>::mma(o[i], pa[0], pa[1], pa[2], pa[3], b0, b1);
+                Pair<T>::mma(o[i + 1], pa[0], pa[1], pa[2], pa[3], b2, b3);
+            }
+        }
+        if (m.flags & kLast) {
+            // ---- join the four warps' parts, each in the stage it has just consumed
+            __syncwarp();
+            float* part = (float*)(ring + (size_t)(warp * kStages + stage) * S::kStage);
+#pragma unroll
+            for (int r = 0; r < (kWide ? 2 : 1); ++r) {
+                float l = l_run[r];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                const int row = gid + 8 * r;
+                if (tig == 0) sh_stat[warp][row] = make_float2(m_run[r], l);
+#pragma unroll
+                for (int i = 0; i < kNt; ++i) {
+                    const float x = kWide ? o[i][2 * r] : o[i][0] + o[i][2];
+                    const float y = kWide ? o[i][2 * r + 1] : o[i][1] + o[i][3];
+                    *(float2*)(part + row * D + ((i * 8 + 2 * tig) ^ ((row & 3) << 3))) = make_float2(x, y);
+                }
+            }
+            __syncthreads();
+            const int slot = 2 * cta + (segment ? 1 : 0);
+            const bool whole = m.flags & kWhole;
+            for (int e = tid; e < nq * D; e += kThreads) {
+                const int row = e / D, col = e % D;
+                float top = kLowest;
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) top = fmaxf(top, sh_stat[x][row].x);
+                float l = 0.f, val = 0.f;
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) {
+                    const float2 st = sh_stat[x][row];
+                    const float f = ptx::ex2(st.x - top);
+                    l += f * st.y;
+                    val += f * ((const float*)(ring + (size_t)(x * kStages + stage) * S::kStage))[row * D + (col ^ ((row & 3) << 3))];
+                }
+                top -= Pair<T>::kBias;         // the sum and the output are 2^kBias larger
+                const size_t query = (size_t)head * a.G + g0 + row;
+                if (whole) {
+                    const float inv = l == 0.f ? 0.f : 1.f / l;     // a NaN sum stays one
+                    ((T*)a.out)[query * D + col] = T(val * inv);
+                    if (col == 0) {
+                        const float lse2 = top + log2f(l);          // -inf where l is 0
+                        if (a.lse) a.lse[query] = lse2 * kLn2;
+                        if (a.logits) a.lse2[query] = lse2;
+                    }
+                } else {
+                    a.parts[((size_t)slot * a.gq + row) * D + col] = val;
+                    if (col == 0) a.stats[(size_t)slot * a.gq + row] = make_float2(top, l);
+                }
+            }
+            __syncthreads();
+            segment = 1;
+        }
+    }
+}
+
+// The parts of the unit whose tiles are [first, first + nt): one a CTA, from c0 to c1.
+struct Parts {
+    int c0, n;
+    bool later;          // c0's run begins before the unit: its part is that CTA's second
+
+    __device__ __forceinline__ Parts(long long first, int nt, long long T, int parties) {
+        c0 = cutter_of(first, T, parties);
+        n = cutter_of(first + nt - 1, T, parties) - c0 + 1;
+        later = cut(c0, T, parties) < first;
+    }
+    __device__ __forceinline__ size_t slot(int i) const { return 2 * (size_t)(c0 + i) + (i == 0 && later ? 1 : 0); }
+};
+
+// The sum of a unit's parts over query head `row`: its log-sum-exp, by one warp.
+__device__ __forceinline__ float joined_lse2(const AttendArgs& a, const Parts& p, int row) {
+    const int lane = threadIdx.x & 31;
+    float top = kLowest;
+    for (int i = lane; i < p.n; i += 32) top = fmaxf(top, a.stats[p.slot(i) * a.gq + row].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float l = 0.f;
+    for (int i = lane; i < p.n; i += 32) {
+        const float2 st = a.stats[p.slot(i) * a.gq + row];
+        l += st.y * ptx::ex2(st.x - top);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    return top + log2f(l);
+}
+
+// Blocks [0, units): a unit each, its output if its parts lie with several CTAs. Blocks from there
+// on: the same runs of tiles as attend_split's CTAs, their rows' weights added to acc.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendArgs a, int units, int split_grid) {
+    __shared__ float sh_lse2[kMaxCacheGroup];
+    ptx::grid_dependency_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long total = *a.total;
+    const int parties = parties_of(total, split_grid);
+    if ((int)blockIdx.x < units) {
+        const int unit = blockIdx.x, head = unit / a.ng, g0 = (unit - head * a.ng) * a.gq;
+        const int nq = min(a.gq, a.G - g0), nt = tiles_of(a.c.len(head));
+        const size_t query = (size_t)head * a.G + g0;
+        if (nt == 0) {                        // no rows
+            for (int e = tid; e < nq * D; e += kJoinThreads) ((T*)a.out)[query * D + e] = T(0.f);
+            if (a.lse && tid < nq) a.lse[query + tid] = -INFINITY;
+            return;
+        }
+        const Parts p(a.first[unit], nt, total, parties);
+        if (p.n == 1) return;                 // attend_split has finished it
+        for (int row = warp; row < nq; row += kJoinThreads / 32) {
+            const float x = joined_lse2(a, p, row);
+            if (lane == 0) {
+                sh_lse2[row] = x;
+                if (a.lse) a.lse[query + row] = x * kLn2;
+            }
+        }
+        __syncthreads();
+        for (int e = tid; e < nq * D; e += kJoinThreads) {
+            const int row = e / D, col = e % D;
+            const float x = sh_lse2[row];
+            float val = 0.f;
+            if (x != -INFINITY) {
+                for (int i = 0; i < p.n; ++i) {
+                    const size_t s = p.slot(i) * a.gq + row;
+                    val += a.parts[s * D + col] * ptx::ex2(a.stats[s].x - x);
+                }
+            }
+            ((T*)a.out)[query * D + e] = T(val);
+        }
+        return;
+    }
+    // ---- acc: one thread four rows at a time, all query heads of the head
+    const int cta = blockIdx.x - units;
+    if (cta >= parties) return;
+    long long r = cut(cta, total, parties);
+    const long long r1 = cut(cta + 1, total, parties);
+    Walk w;
+    w.begin(a.c, a.ng, a.starts[cta]);
+    const int cap = a.c.cap();
+    while (true) {
+        const int here = (int)min((long long)(w.nt - w.tile), r1 - r);   // tiles of this unit in the run
+        if (w.sub == 0) {
+            __syncthreads();                  // the unit before has been read
+            for (int g = warp; g < a.G; g += kJoinThreads / 32) {
+                const int unit = w.head * a.ng + g / a.gq;
+                const Parts p(a.first[unit], w.nt, total, parties);
+                const float x = p.n == 1 ? a.lse2[(size_t)w.head * a.G + g] : joined_lse2(a, p, g % a.gq);
+                if (lane == 0) sh_lse2[g] = x;
+            }
+            __syncthreads();
+            const int last = min(w.len, (w.tile + here) * kTile);
+            const float* lp = a.logits + (size_t)w.head * a.G * cap;
+            for (int j = w.tile * kTile + tid * 4; j < last; j += kJoinThreads * 4) {
+                const long long row = a.c.row(w.head, j);                // four rows lie in one page
+                if (row < 0) continue;
+                float s[4] = {};
+                for (int g = 0; g < a.G; ++g) {
+                    const float4 t = *(const float4*)(lp + (size_t)g * cap + j);
+                    const float x = sh_lse2[g];
+                    if (x == -INFINITY) continue;
+                    s[0] += ptx::ex2(t.x - x);
+                    s[1] += ptx::ex2(t.y - x);
+                    s[2] += ptx::ex2(t.z - x);
+                    s[3] += ptx::ex2(t.w - x);
+                }
+                if (!KVP_CHECK(row + 3 < ((long long)a.c.num_pages << a.c.page_shift), 601, w.head, j)) continue;
+                float* ap = a.acc + row;
+                if (j + 4 <= last) {
+                    float4 x = *(float4*)ap;
+                    x.x += s[0];
+                    x.y += s[1];
+                    x.z += s[2];
+                    x.w += s[3];
+                    *(float4*)ap = x;
+                } else {
+                    for (int i = 0; j + i < last; ++i) ap[i] += s[i];
+                }
+            }
+        }
+        r += here;
+        if (r >= r1) break;
+        w.tile += here - 1;
+        w.next(a.c, a.ng);
+    }
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Layout {
+    int ng, gq, units, grid;
+    size_t starts, total, first, stats, parts, lse2, logits, bytes;
+};
+
+// bytes = 0: more tiles than the kernels count in 32 bits.
+Layout layout_of(const kvp_cache_shape& s, bool accumulate) {
+    Layout l = {};
+    const int G = s.hq / s.hkv, d = s.head_dim;
+    const long long heads = (long long)s.batch * s.hkv, cap = (long long)s.max_pages * s.page_size;
+    l.gq = G <= 8 ? 8 : 16;
+    l.ng = (G + l.gq - 1) / l.gq;
+    if (heads * l.ng * ((cap + kTile - 1) / kTile) > INT32_MAX) return l;
+    l.units = (int)(heads * l.ng);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += align256(bytes);
+        return here;
+    };
+    l.total = take(sizeof(long long));
+    l.starts = take(kMaxGrid * sizeof(Start));
+    l.first = take((size_t)l.units * sizeof(uint32_t));
+    l.stats = take((size_t)2 * kMaxGrid * l.gq * sizeof(float2));
+    l.parts = take((size_t)2 * kMaxGrid * l.gq * d * sizeof(float));
+    if (accumulate) {
+        l.lse2 = take((size_t)heads * G * sizeof(float));
+        l.logits = take((size_t)heads * G * cap * sizeof(float));
+    }
+    l.bytes = at;
+    return l;
+}
+
+template <typename T, int D, bool kWide, int kStages>
+cudaError_t launch_split(const AttendArgs& a, int grid, cudaStream_t st) {
+    auto kernel = attend_split<T, D, kWide, kStages>;
+    constexpr size_t smem = Split<T, D, kWide, kStages>::kSmem;
+    const cudaError_t e = allow_dynamic_smem((const void*)kernel, smem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kernel, grid, kThreads, smem, st, a);
+}
+
+template <typename T, int D>
+cudaError_t launch_both(const AttendArgs& a, const Layout& l, int grid, cudaStream_t st) {
+    constexpr int kStages = D == 128 ? 3 : 6;
+    const cudaError_t e = a.gq == 16 ? launch_split<T, D, true, kStages>(a, grid, st)
+                                     : launch_split<T, D, false, kStages>(a, grid, st);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(attend_join<T, D>, l.units + (a.acc ? grid : 0), kJoinThreads, 0, st, a, l.units, grid);
+}
+
+}  // namespace
+
+size_t attend_workspace_bytes(const kvp_cache_shape& s, bool accumulate) { return layout_of(s, accumulate).bytes; }
+
+cudaError_t launch_attend(const kvp_cache_shape& s, const uint16_t* q, const uint16_t* k_pages,
+                          const uint16_t* v_pages, const int32_t* table, const int32_t* lens, uint16_t* out,
+                          float* lse, float* acc, void* workspace, cudaStream_t st) {
+    const Layout l = layout_of(s, acc != nullptr);
+    char* ws = (char*)workspace;
+    AttendArgs a;
+    a.c = cache_view(s, table, lens);
+    a.q = q;
+    a.k = k_pages;
+    a.v = v_pages;
+    a.out = out;
+    a.lse = lse;
+    a.acc = acc;
+    a.G = s.hq / s.hkv;
+    a.ng = l.ng;
+    a.gq = l.gq;
+    a.scale2 = (float)(1.4426950408889634 / sqrt((double)s.head_dim));
+    a.starts = (Start*)(ws + l.starts);
+    a.total = (long long*)(ws + l.total);
+    a.first = (uint32_t*)(ws + l.first);
+    a.stats = (float2*)(ws + l.stats);
+    a.parts = (float*)(ws + l.parts);
+    a.lse2 = acc ? (float*)(ws + l.lse2) : nullptr;
+    a.logits = acc ? (float*)(ws + l.logits) : nullptr;
+    const int grid = std::min(num_sms(), kPlanGrid) * kCtasPerSm;
+    if (s.dtype == KVP_BF16)
+        return s.head_dim == 128 ? launch_both<__nv_bfloat16, 128>(a, l, grid, st)
+                                 : launch_both<__nv_bfloat16, 64>(a, l, grid, st);
+    return s.head_dim == 128 ? launch_both<__half, 128>(a, l, grid, st) : launch_both<__half, 64>(a, l, grid, st);
+}
+
+#ifdef KVP_CHECKS
+KVP_DEFINE_CHECK_READER(take_check_attend)
+#endif
+
+}  // namespace kvp

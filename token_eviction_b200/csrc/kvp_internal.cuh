@@ -178,6 +178,9 @@ int take_check_select(int* out4);
 int take_check_compact(int* out4);
 int take_check_leverage(int* out4);
 int take_check_adaptive(int* out4);
+int take_check_append(int* out4);
+int take_check_attend(int* out4);
+int take_check_evict(int* out4);
 static __device__ __noinline__ void kvp_check_fail(int code, int a, int b) {
     if (atomicCAS(&g_kvp_check[0], 0, code) == 0) {
         g_kvp_check[1] = a;
