@@ -14,9 +14,11 @@
 // softmax, and never waits for another warp until the unit ends. There the four warps' parts
 // are joined in shared memory; a unit that lies within one CTA is finished, others leave a part
 // (unnormalised output, maximum, sum) in the workspace.
-// attend_join: joins the parts of the units that were cut, in the order of the rows, and adds
-// the attention weights to acc, from the logits that attend_split left in the workspace (4 G
-// bytes a row against 4 d of the row itself, most of them still in L2).
+// attend_join: joins the parts of the units that were cut (a CTA has two at most), in the order of
+// the rows.
+// The weights that acc gains need the final sum, so the logits go through the workspace (4 G bytes
+// a row against 4 d of the row itself) and are read back, mostly from L2, by the CTA that finished
+// the unit, or by attend_join for units that were cut.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,7 +36,8 @@ constexpr int kGroup = 16;                        // rows a warp takes at a time
 constexpr int kTile = kWarps * kGroup;            // rows a CTA takes at a time
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxGrid = kPlanGrid * kCtasPerSm;  // the workspace holds parts for as many CTAs
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinPieces = 4;                    // blocks of attend_join that share one part
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.4028234663852886e38f;  // of a maximum over nothing: finite, so that
                                                     // differences of maxima are never inf - inf
@@ -42,6 +45,15 @@ constexpr float kLowest = -3.4028234663852886e38f;  // of a maximum over nothing
 // Where a CTA's run begins: its unit, the tile within it.
 struct Start {
     int unit, tile;
+};
+
+// A CTA's share of a unit that other CTAs share too: tiles [tile, tile + count) of the unit. Its
+// n parts are those of CTAs c0 .. c0 + n - 1: c0's last unit if `later`, the first of the others.
+struct Cut {
+    int unit, tile, count, head;       // unit = -1: no such share
+    int c0, n, later, len;
+
+    __device__ __forceinline__ size_t slot(int i) const { return 2 * (size_t)(c0 + i) + (i == 0 && later ? 1 : 0); }
 };
 
 struct AttendArgs {
@@ -55,12 +67,10 @@ struct AttendArgs {
     int G, ng, gq;       // query heads per head; units per head; query heads per unit (the last: fewer)
     float scale2;        // log2 e / sqrt(d)
     // workspace
-    Start* starts;       // [grid]
-    long long* total;    // tiles
-    uint32_t* first;     // [units]: the unit's first tile
+    Cut* cuts;           // [2 grid]: what each CTA's first and last unit had of it, where they were cut
     float2* stats;       // [2 grid][gq]: a part's maximum and sum, log2 domain
     float* parts;        // [2 grid][gq][d]: a part's unnormalised output
-    float* lse2;         // [heads * G]: of units that were not cut
+    float* lse2;         // [heads * G], with acc and more than one unit a head
     float* logits;       // [heads * G][cap], log2 domain; NULL without acc
 };
 
@@ -140,6 +150,42 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// acc += the weights of rows [j0, j1) of `head` (j0 a multiple of 4), from their logits: one thread
+// four rows at a time. lse2[g] = +inf where query head g has no weights to give.
+template <int kStride>
+__device__ __forceinline__ void add_weights(const AttendArgs& a, int head, int j0, int j1, int tid, const float* lse2) {
+    const int cap = a.c.cap();
+    for (int j = j0 + tid * 4; j < j1; j += kStride * 4) {
+        const long long row = a.c.row(head, j);              // four rows lie in one page
+        if (row < 0) continue;
+        const float* lp = a.logits + (size_t)head * a.G * cap + j;
+        float* ap = a.acc + row;
+        if (!KVP_CHECK(row + 3 < ((long long)a.c.num_pages << a.c.page_shift), 601, head, j)) continue;
+        float4 x = *(const float4*)ap;                       // (the page's next rows past the last one)
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll 4
+        for (int g = 0; g < a.G; ++g) {
+            const float4 t = *(const float4*)(lp + (size_t)g * cap);
+            const float l = lse2[g];
+            s0 += ptx::ex2(t.x - l);
+            s1 += ptx::ex2(t.y - l);
+            s2 += ptx::ex2(t.z - l);
+            s3 += ptx::ex2(t.w - l);
+        }
+        x.x += s0;
+        x.y += s1;
+        x.z += s2;
+        x.w += s3;
+        if (j + 4 <= j1) {
+            *(float4*)ap = x;
+        } else {
+            ap[0] = x.x;
+            if (j + 1 < j1) ap[1] = x.y;
+            if (j + 2 < j1) ap[2] = x.z;
+        }
+    }
 }
 
 // Where tile `want` of the run lies: every thread of the CTA sums a stretch of heads' tiles, and
@@ -260,18 +306,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
     __shared__ Start at;
     __shared__ Meta meta[kWarps][kStages];
     __shared__ float2 sh_stat[kWarps][kQ];
+    __shared__ float sh_lse2[kQ];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gid = lane >> 2, tig = lane & 3;
     const int grid = gridDim.x, cta = blockIdx.x;
 
     ptx::grid_dependency_wait();
     const long long T_ = find_start(a.c, a.ng, grid, cta, warp_sums, &at);
+    ptx::launch_dependents();
+    // heads without rows
+    for (int h = cta; h < a.c.heads; h += grid) {
+        if (a.c.len(h) > 0) continue;
+        for (int e = tid; e < a.G * D; e += kThreads) ((T*)a.out)[(size_t)h * a.G * D + e] = T(0.f);
+        if (a.lse && tid < a.G) a.lse[(size_t)h * a.G + tid] = -INFINITY;
+    }
     const int parties = parties_of(T_, grid);
-    if (tid == 0 && cta == 0) *a.total = T_;
+    if (tid < 2) a.cuts[2 * cta + tid].unit = -1;
     if (cta >= parties) return;
     const long long r0 = cut(cta, T_, parties);
     const int steps = (int)(cut(cta + 1, T_, parties) - r0);
-    if (tid == 0) a.starts[cta] = at;
 
     // ---- the issuing side: one group ahead of its loads, so that its page is at hand
     Walk w;
@@ -303,8 +356,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
                 m.flags = (fresh ? kFirst : 0) | (last ? kLast : 0) |
                           (last && begins && w.tile == w.nt - 1 ? kWhole : 0);
                 meta[warp][stage] = m;
-                // the unit's place in the run, for the join
-                if (warp == 0 && w.tile == 0) a.first[m.unit] = (uint32_t)(r0 + issued);
             }
             if (valid > 0) {
                 const size_t row = ((size_t)page << a.c.page_shift) + (row0 & ((1 << a.c.page_shift) - 1));
@@ -343,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
     uint32_t qf[D / 16][kWide ? 4 : 2];
     const int b_row = (lane & 7) + ((lane >> 4) & 1) * 8, b_chunk = (lane >> 3) & 1;   // keys
     const int v_row = (lane & 7) + ((lane >> 3) & 1) * 8, v_chunk = (lane >> 4) & 1;   // values
-    int segment = 0;
+    int segment = 0, seg_step = 0;            // units begun before this one; the step that began it
 
     for (int step = 0; step < steps; ++step) {
         const int stage = step % kStages;
@@ -355,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
         const int head = m.unit / a.ng, g0 = (m.unit - head * a.ng) * a.gq;
         const int nq = min(a.gq, a.G - g0);   // query heads of this unit
         if (m.flags & kFirst) {
+            seg_step = step;
 #pragma unroll
             for (int i = 0; i < kNt; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
             m_run[0] = m_run[1] = kLowest;
@@ -482,34 +534,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
                     if (col == 0) {
                         const float lse2 = top + log2f(l);          // -inf where l is 0
                         if (a.lse) a.lse[query] = lse2 * kLn2;
-                        if (a.logits) a.lse2[query] = lse2;
+                        if (a.lse2) a.lse2[query] = lse2;
+                        sh_lse2[row] = l == 0.f ? INFINITY : lse2;
                     }
                 } else {
                     a.parts[((size_t)slot * a.gq + row) * D + col] = val;
                     if (col == 0) a.stats[(size_t)slot * a.gq + row] = make_float2(top, l);
                 }
             }
+            if (!whole && tid == 0) {
+                Cut x;
+                const int tile = m.row0 / kTile - (step - seg_step);   // the share's first
+                x.unit = m.unit;
+                x.head = head;
+                x.tile = tile;
+                x.count = step - seg_step + 1;
+                x.len = a.c.len(head);
+                const long long first = r0 + seg_step - tile;          // the unit's first tile in the run
+                x.c0 = cutter_of(first, T_, parties);
+                x.n = cutter_of(first + tiles_of(x.len) - 1, T_, parties) - x.c0 + 1;
+                x.later = cut(x.c0, T_, parties) < first;
+                a.cuts[slot] = x;
+            }
             __syncthreads();
+            if (whole && a.logits && a.ng == 1)
+                add_weights<kThreads>(a, head, 0, a.c.len(head), tid, sh_lse2);
             segment = 1;
         }
     }
 }
 
-// The parts of the unit whose tiles are [first, first + nt): one a CTA, from c0 to c1.
-struct Parts {
-    int c0, n;
-    bool later;          // c0's run begins before the unit: its part is that CTA's second
-
-    __device__ __forceinline__ Parts(long long first, int nt, long long T, int parties) {
-        c0 = cutter_of(first, T, parties);
-        n = cutter_of(first + nt - 1, T, parties) - c0 + 1;
-        later = cut(c0, T, parties) < first;
-    }
-    __device__ __forceinline__ size_t slot(int i) const { return 2 * (size_t)(c0 + i) + (i == 0 && later ? 1 : 0); }
-};
-
-// The sum of a unit's parts over query head `row`: its log-sum-exp, by one warp.
-__device__ __forceinline__ float joined_lse2(const AttendArgs& a, const Parts& p, int row) {
+// log2 of the sum of a unit's parts over query head `row`, by one warp.
+__device__ __forceinline__ float joined_lse2(const AttendArgs& a, const Cut& p, int row) {
     const int lane = threadIdx.x & 31;
     float top = kLowest;
     for (int i = lane; i < p.n; i += 32) top = fmaxf(top, a.stats[p.slot(i) * a.gq + row].x);
@@ -525,108 +581,99 @@ __device__ __forceinline__ float joined_lse2(const AttendArgs& a, const Parts& p
     return top + log2f(l);
 }
 
-// Blocks [0, units): a unit each, its output if its parts lie with several CTAs. Blocks from there
-// on: the same runs of tiles as attend_split's CTAs, their rows' weights added to acc.
+// kJoinPieces blocks for each share of a cut unit: its rows' weights go to acc, and the blocks of
+// the unit's first share join its output, a query head each at a time.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendArgs a, int units, int split_grid) {
-    __shared__ float sh_lse2[kMaxCacheGroup];
+__global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendArgs a) {
+    constexpr int kCols = D / 32;             // columns a lane joins
+    __shared__ float sh_lse2[16];
+    __shared__ float sh_val[kJoinWarps][D];
     ptx::grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long total = *a.total;
-    const int parties = parties_of(total, split_grid);
-    if ((int)blockIdx.x < units) {
-        const int unit = blockIdx.x, head = unit / a.ng, g0 = (unit - head * a.ng) * a.gq;
-        const int nq = min(a.gq, a.G - g0), nt = tiles_of(a.c.len(head));
-        const size_t query = (size_t)head * a.G + g0;
-        if (nt == 0) {                        // no rows
-            for (int e = tid; e < nq * D; e += kJoinThreads) ((T*)a.out)[query * D + e] = T(0.f);
-            if (a.lse && tid < nq) a.lse[query + tid] = -INFINITY;
-            return;
-        }
-        const Parts p(a.first[unit], nt, total, parties);
-        if (p.n == 1) return;                 // attend_split has finished it
-        for (int row = warp; row < nq; row += kJoinThreads / 32) {
+    const int slot = blockIdx.x / kJoinPieces, piece = blockIdx.x % kJoinPieces;
+    const Cut p = a.cuts[slot];
+    if (p.unit < 0) return;
+    const int g0 = (p.unit - p.head * a.ng) * a.gq, nq = min(a.gq, a.G - g0);
+    const bool weigh = a.logits && a.ng == 1, joins = p.tile == 0;
+    if (weigh || joins) {
+        for (int row = warp; row < nq; row += kJoinWarps) {
             const float x = joined_lse2(a, p, row);
-            if (lane == 0) {
-                sh_lse2[row] = x;
-                if (a.lse) a.lse[query + row] = x * kLn2;
-            }
+            if (lane == 0) sh_lse2[row] = x;
         }
-        __syncthreads();
-        for (int e = tid; e < nq * D; e += kJoinThreads) {
-            const int row = e / D, col = e % D;
+    }
+    __syncthreads();
+    if (joins) {
+        for (int row = piece; row < nq; row += kJoinPieces) {
             const float x = sh_lse2[row];
-            float val = 0.f;
+            const size_t query = (size_t)p.head * a.G + g0 + row;
+            float val[kCols] = {};
             if (x != -INFINITY) {
-                for (int i = 0; i < p.n; ++i) {
+#pragma unroll 4
+                for (int i = warp; i < p.n; i += kJoinWarps) {
                     const size_t s = p.slot(i) * a.gq + row;
-                    val += a.parts[s * D + col] * ptx::ex2(a.stats[s].x - x);
+                    const float f = ptx::ex2(a.stats[s].x - x);
+                    const float* from = a.parts + s * D + lane * kCols;
+                    if constexpr (kCols == 4) {
+                        const float4 y = *(const float4*)from;
+                        val[0] += f * y.x;
+                        val[1] += f * y.y;
+                        val[2] += f * y.z;
+                        val[3] += f * y.w;
+                    } else {
+                        const float2 y = *(const float2*)from;
+                        val[0] += f * y.x;
+                        val[1] += f * y.y;
+                    }
                 }
             }
-            ((T*)a.out)[query * D + e] = T(val);
-        }
-        return;
-    }
-    // ---- acc: one thread four rows at a time, all query heads of the head
-    const int cta = blockIdx.x - units;
-    if (cta >= parties) return;
-    long long r = cut(cta, total, parties);
-    const long long r1 = cut(cta + 1, total, parties);
-    Walk w;
-    w.begin(a.c, a.ng, a.starts[cta]);
-    const int cap = a.c.cap();
-    while (true) {
-        const int here = (int)min((long long)(w.nt - w.tile), r1 - r);   // tiles of this unit in the run
-        if (w.sub == 0) {
-            __syncthreads();                  // the unit before has been read
-            for (int g = warp; g < a.G; g += kJoinThreads / 32) {
-                const int unit = w.head * a.ng + g / a.gq;
-                const Parts p(a.first[unit], w.nt, total, parties);
-                const float x = p.n == 1 ? a.lse2[(size_t)w.head * a.G + g] : joined_lse2(a, p, g % a.gq);
-                if (lane == 0) sh_lse2[g] = x;
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) sh_val[warp][lane * kCols + i] = val[i];
+            __syncthreads();
+            if (tid < D) {
+                float sum = 0.f;
+#pragma unroll
+                for (int y = 0; y < kJoinWarps; ++y) sum += sh_val[y][tid];
+                ((T*)a.out)[query * D + tid] = T(sum);
+                if (tid == 0) {
+                    if (a.lse) a.lse[query] = x * kLn2;
+                    if (a.lse2) a.lse2[query] = x;
+                }
             }
             __syncthreads();
-            const int last = min(w.len, (w.tile + here) * kTile);
-            const float* lp = a.logits + (size_t)w.head * a.G * cap;
-            for (int j = w.tile * kTile + tid * 4; j < last; j += kJoinThreads * 4) {
-                const long long row = a.c.row(w.head, j);                // four rows lie in one page
-                if (row < 0) continue;
-                float s[4] = {};
-                for (int g = 0; g < a.G; ++g) {
-                    const float4 t = *(const float4*)(lp + (size_t)g * cap + j);
-                    const float x = sh_lse2[g];
-                    if (x == -INFINITY) continue;
-                    s[0] += ptx::ex2(t.x - x);
-                    s[1] += ptx::ex2(t.y - x);
-                    s[2] += ptx::ex2(t.z - x);
-                    s[3] += ptx::ex2(t.w - x);
-                }
-                if (!KVP_CHECK(row + 3 < ((long long)a.c.num_pages << a.c.page_shift), 601, w.head, j)) continue;
-                float* ap = a.acc + row;
-                if (j + 4 <= last) {
-                    float4 x = *(float4*)ap;
-                    x.x += s[0];
-                    x.y += s[1];
-                    x.z += s[2];
-                    x.w += s[3];
-                    *(float4*)ap = x;
-                } else {
-                    for (int i = 0; j + i < last; ++i) ap[i] += s[i];
-                }
-            }
         }
-        r += here;
-        if (r >= r1) break;
-        w.tile += here - 1;
-        w.next(a.c, a.ng);
     }
+    if (weigh) {
+        if (tid < nq && sh_lse2[tid] == -INFINITY) sh_lse2[tid] = INFINITY;
+        __syncthreads();
+        // rows of this share, dealt to its blocks kJoinThreads * 4 at a time
+        const int last = min(p.len, (p.tile + p.count) * kTile);
+        for (int j = p.tile * kTile + piece * kJoinThreads * 4; j < last; j += kJoinPieces * kJoinThreads * 4)
+            add_weights<kJoinThreads>(a, p.head, j, min(last, j + kJoinThreads * 4), tid, sh_lse2);
+    }
+}
+
+// acc += the weights, for heads whose query heads are several units (G > 16): `per` blocks a head,
+// once all of its sums are known.
+__global__ void __launch_bounds__(kJoinThreads) attend_weigh(const AttendArgs a, int per) {
+    __shared__ float sh_lse2[kMaxCacheGroup];
+    ptx::grid_dependency_wait();
+    const int head = blockIdx.x / per, len = a.c.len(head);
+    if (len == 0) return;
+    for (int g = threadIdx.x; g < a.G; g += kJoinThreads) {
+        const float x = a.lse2[(size_t)head * a.G + g];
+        sh_lse2[g] = x == -INFINITY ? INFINITY : x;
+    }
+    __syncthreads();
+    constexpr int kRows = kJoinThreads * 4;
+    for (int j = blockIdx.x % per * kRows; j < len; j += per * kRows)
+        add_weights<kJoinThreads>(a, head, j, min(len, j + kRows), threadIdx.x, sh_lse2);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
-    int ng, gq, units, grid;
-    size_t starts, total, first, stats, parts, lse2, logits, bytes;
+    int ng, gq;
+    size_t cuts, stats, parts, lse2, logits, bytes;
 };
 
 // bytes = 0: more tiles than the kernels count in 32 bits.
@@ -637,20 +684,17 @@ Layout layout_of(const kvp_cache_shape& s, bool accumulate) {
     l.gq = G <= 8 ? 8 : 16;
     l.ng = (G + l.gq - 1) / l.gq;
     if (heads * l.ng * ((cap + kTile - 1) / kTile) > INT32_MAX) return l;
-    l.units = (int)(heads * l.ng);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
         at += align256(bytes);
         return here;
     };
-    l.total = take(sizeof(long long));
-    l.starts = take(kMaxGrid * sizeof(Start));
-    l.first = take((size_t)l.units * sizeof(uint32_t));
+    l.cuts = take((size_t)2 * kMaxGrid * sizeof(Cut));
     l.stats = take((size_t)2 * kMaxGrid * l.gq * sizeof(float2));
     l.parts = take((size_t)2 * kMaxGrid * l.gq * d * sizeof(float));
     if (accumulate) {
-        l.lse2 = take((size_t)heads * G * sizeof(float));
+        if (l.ng > 1) l.lse2 = take((size_t)heads * G * sizeof(float));
         l.logits = take((size_t)heads * G * cap * sizeof(float));
     }
     l.bytes = at;
@@ -667,12 +711,15 @@ cudaError_t launch_split(const AttendArgs& a, int grid, cudaStream_t st) {
 }
 
 template <typename T, int D>
-cudaError_t launch_both(const AttendArgs& a, const Layout& l, int grid, cudaStream_t st) {
+cudaError_t launch_all(const AttendArgs& a, int grid, cudaStream_t st) {
     constexpr int kStages = D == 128 ? 3 : 6;
-    const cudaError_t e = a.gq == 16 ? launch_split<T, D, true, kStages>(a, grid, st)
+    cudaError_t e = a.gq == 16 ? launch_split<T, D, true, kStages>(a, grid, st)
                                      : launch_split<T, D, false, kStages>(a, grid, st);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attend_join<T, D>, l.units + (a.acc ? grid : 0), kJoinThreads, 0, st, a, l.units, grid);
+    e = launch_dependent(attend_join<T, D>, 2 * grid * kJoinPieces, kJoinThreads, 0, st, a);
+    if (e != cudaSuccess || !a.lse2) return e;
+    const int per = std::max(1, std::min(num_sms() * 8 / a.c.heads, (a.c.cap() + kJoinThreads * 4 - 1) / (kJoinThreads * 4)));
+    return launch_dependent(attend_weigh, a.c.heads * per, kJoinThreads, 0, st, a, per);
 }
 
 }  // namespace
@@ -696,18 +743,16 @@ cudaError_t launch_attend(const kvp_cache_shape& s, const uint16_t* q, const uin
     a.ng = l.ng;
     a.gq = l.gq;
     a.scale2 = (float)(1.4426950408889634 / sqrt((double)s.head_dim));
-    a.starts = (Start*)(ws + l.starts);
-    a.total = (long long*)(ws + l.total);
-    a.first = (uint32_t*)(ws + l.first);
+    a.cuts = (Cut*)(ws + l.cuts);
     a.stats = (float2*)(ws + l.stats);
     a.parts = (float*)(ws + l.parts);
-    a.lse2 = acc ? (float*)(ws + l.lse2) : nullptr;
+    a.lse2 = acc && l.ng > 1 ? (float*)(ws + l.lse2) : nullptr;
     a.logits = acc ? (float*)(ws + l.logits) : nullptr;
     const int grid = std::min(num_sms(), kPlanGrid) * kCtasPerSm;
     if (s.dtype == KVP_BF16)
-        return s.head_dim == 128 ? launch_both<__nv_bfloat16, 128>(a, l, grid, st)
-                                 : launch_both<__nv_bfloat16, 64>(a, l, grid, st);
-    return s.head_dim == 128 ? launch_both<__half, 128>(a, l, grid, st) : launch_both<__half, 64>(a, l, grid, st);
+        return s.head_dim == 128 ? launch_all<__nv_bfloat16, 128>(a, grid, st)
+                                 : launch_all<__nv_bfloat16, 64>(a, grid, st);
+    return s.head_dim == 128 ? launch_all<__half, 128>(a, grid, st) : launch_all<__half, 64>(a, grid, st);
 }
 
 #ifdef KVP_CHECKS

@@ -234,6 +234,12 @@ __device__ __forceinline__ void grid_dependency_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Lets the grid that depends on this one launch once every block has called this or exited; it
+// still waits (grid_dependency_wait) for this grid's end before it reads what this one writes.
+__device__ __forceinline__ void launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Makes this thread's ordinary (generic-proxy) writes to shared memory visible to the
 // async proxy: operands the tensor cores read through descriptors.
 __device__ __forceinline__ void fence_proxy_async_smem() {
