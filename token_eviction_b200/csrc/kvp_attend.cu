@@ -71,7 +71,7 @@ struct AttendArgs {
     float2* stats;       // [2 grid][gq]: a part's maximum and sum, log2 domain
     float* parts;        // [2 grid][gq][d]: a part's unnormalised output
     float* lse2;         // [heads * G], with acc and more than one unit a head
-    float* logits;       // [heads * G][cap], log2 domain; NULL without acc
+    float* logits;       // [heads * G][cap]: q . k; NULL without acc
 };
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
@@ -142,9 +142,14 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t& r0, uint32_t& r1
                  : "r"(addr)
                  : "memory");
 }
-// 16 bytes global -> shared, or 16 zero bytes when `bytes` is 0.
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// 16 bytes global -> shared.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
+                 : "memory");
+}
+// The same, or 16 zero bytes (src is not read).
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -169,10 +174,10 @@ __device__ __forceinline__ void add_weights(const AttendArgs& a, int head, int j
         for (int g = 0; g < a.G; ++g) {
             const float4 t = *(const float4*)(lp + (size_t)g * cap);
             const float l = lse2[g];
-            s0 += ptx::ex2(t.x - l);
-            s1 += ptx::ex2(t.y - l);
-            s2 += ptx::ex2(t.z - l);
-            s3 += ptx::ex2(t.w - l);
+            s0 += ptx::ex2(fmaf(t.x, a.scale2, -l));
+            s1 += ptx::ex2(fmaf(t.y, a.scale2, -l));
+            s2 += ptx::ex2(fmaf(t.z, a.scale2, -l));
+            s3 += ptx::ex2(fmaf(t.w, a.scale2, -l));
         }
         x.x += s0;
         x.y += s1;
@@ -275,17 +280,20 @@ struct Walk {
 };
 
 // What a warp notes about a group when it issues its loads and reads when it consumes it.
-struct Meta {
-    int unit, row0;      // the group's first row within the head
-    int valid;           // rows of it that are there (0: nothing was loaded)
-    int flags;           // kFirst, kLast: of the unit, within this CTA's run; kWhole: the run has all of the unit
+struct __align__(16) Meta {
+    int head, sub;       // the unit
+    int row0;            // the group's first row within the head
+    int valid_flags;     // rows of it that are there (0: nothing was loaded), and flags
 };
-constexpr int kFirst = 1, kLast = 2, kWhole = 4;
+// kFirst, kLast: of the unit, within this CTA's run; kWhole: the run has all of the unit
+constexpr int kFirst = 32, kLast = 64, kWhole = 128, kValid = 31;
 
 // Elements: T. D: head dimension. kWide: up to 16 query heads a unit, one row each of the MMA's
 // 16; else up to 8, whose weights fill rows 0-7 and the remainders left by rounding them to T
 // rows 8-15: the product with V then carries about twice T's precision, for free, since the
 // MMA has 16 rows anyway.
+constexpr uint32_t kRingAlign = 256;      // rows of 256 bytes: a chunk's bits of an address are free for xor
+
 template <typename T, int D, bool kWide, int kStages>
 struct Split {
     static constexpr int kRowBytes = D * 2;
@@ -293,7 +301,7 @@ struct Split {
     static constexpr int kHalf = kGroup * kRowBytes;            // a group's keys (then its values)
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kQ = kWide ? 16 : 8;                   // query heads a unit
-    static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage;
+    static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage + kRingAlign;
     static_assert(kQ * D * 4 <= kStage, "a warp's part is joined in the stage it has consumed");
 };
 
@@ -301,7 +309,8 @@ template <typename T, int D, bool kWide, int kStages>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const AttendArgs a) {
     using S = Split<T, D, kWide, kStages>;
     constexpr int kRowBytes = S::kRowBytes, kQ = S::kQ;
-    extern __shared__ __align__(128) uint8_t ring[];
+    extern __shared__ __align__(16) uint8_t raw[];
+    uint8_t* const ring = raw + (-ptx::smem_u32(raw) & (kRingAlign - 1));
     __shared__ long long warp_sums[kWarps];
     __shared__ Start at;
     __shared__ Meta meta[kWarps][kStages];
@@ -326,60 +335,81 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
     const long long r0 = cut(cta, T_, parties);
     const int steps = (int)(cut(cta + 1, T_, parties) - r0);
 
-    // ---- the issuing side: one group ahead of its loads, so that its page is at hand
+    // ---- the issuing side: the walk is one tile ahead of its loads, so that its page is at hand
     Walk w;
     w.begin(a.c, a.ng, at);
     const uint32_t my_ring = ptx::smem_u32(ring) + warp * kStages * S::kStage;
-    auto page_of = [&]() -> int {            // of the walk's current group; -1: nothing to load
-        const int row0 = w.tile * kTile + warp * kGroup;
-        if (row0 >= w.len) return -1;
-        const int p = a.c.table[(size_t)w.head * a.c.max_pages + (row0 >> a.c.page_shift)];
-        return p < 0 || p >= a.c.num_pages ? -1 : p;
+    // pages of the walk's unit, a lane each: of this warp's groups in tiles [page_base, page_base + 32)
+    int page_base = 0, pages = -1;
+    auto load_pages = [&]() {
+        page_base = w.tile;
+        const int row0 = (page_base + lane) * kTile + warp * kGroup;
+        pages = -1;
+        if (row0 < w.len) {
+            const int p = a.c.table[(size_t)w.head * a.c.max_pages + (row0 >> a.c.page_shift)];
+            if (p < a.c.num_pages) pages = p;
+        }
     };
-    int issued = 0, page = page_of();
+    load_pages();
+    int issued = 0, fill = 0;                // groups issued; the stage the next one goes to
+    const uint64_t stream = ptx::policy_evict_first();   // rows are read once; what L2 holds better is the logits
     bool fresh = true;                       // the walk's tile is the run's first of its unit
     bool begins = w.tile == 0;               // and the unit's first
-    // lanes of a load: kChunks lanes to a row, so 32 / kChunks rows at a time
+    // lanes of a load: kChunks lanes to a row, kRowsAt rows at a time. A row's chunks are stored
+    // xor (row & 7), so that eight rows' same chunk lies in eight bank groups.
     constexpr int kRowsAt = 32 / S::kChunks;
     const int chunk = lane % S::kChunks, lrow = lane / S::kChunks;
+    const uint8_t* k_lane = (const uint8_t*)a.k + lrow * kRowBytes + chunk * 16;
+    const uint8_t* v_lane = (const uint8_t*)a.v + lrow * kRowBytes + chunk * 16;
+    const uint32_t dst_lane = my_ring + lrow * kRowBytes + ((chunk ^ lrow) << 4);   // lrow < kRowsAt <= 4
+    const int page_mask = (1 << a.c.page_shift) - 1;
     auto issue = [&]() {
         if (issued < steps) {
-            const int stage = issued % kStages;
             const int row0 = w.tile * kTile + warp * kGroup;
-            const int valid = page < 0 ? 0 : min(kGroup, w.len - row0);
-            const bool last = w.tile == w.nt - 1 || issued == steps - 1;
+            const int page = __shfl_sync(0xffffffffu, pages, w.tile - page_base);
+            const int valid = page < 0 ? 0 : min(kGroup, w.len - row0);   // (-1 too past the head's rows)
+            const bool ends = w.tile == w.nt - 1;
             if (lane == 0) {
                 Meta m;
-                m.unit = w.head * a.ng + w.sub;
+                m.head = w.head;
+                m.sub = w.sub;
                 m.row0 = row0;
-                m.valid = valid;
-                m.flags = (fresh ? kFirst : 0) | (last ? kLast : 0) |
-                          (last && begins && w.tile == w.nt - 1 ? kWhole : 0);
-                meta[warp][stage] = m;
+                m.valid_flags = valid | (fresh ? kFirst : 0) | (ends || issued == steps - 1 ? kLast : 0) |
+                                (ends && begins ? kWhole : 0);
+                meta[warp][fill] = m;
             }
-            if (valid > 0) {
-                const size_t row = ((size_t)page << a.c.page_shift) + (row0 & ((1 << a.c.page_shift) - 1));
-                const uint8_t* ks = (const uint8_t*)a.k + (row + lrow) * kRowBytes + chunk * 16;
-                const uint8_t* vs = (const uint8_t*)a.v + (row + lrow) * kRowBytes + chunk * 16;
-                const uint32_t dst = my_ring + stage * S::kStage + lrow * kRowBytes;
+            const size_t off = (((size_t)page << a.c.page_shift) + (row0 & page_mask)) * kRowBytes;
+            const uint32_t dst = dst_lane + fill * S::kStage;
+            if (valid == kGroup) {
+                const uint8_t *ks = k_lane + off, *vs = v_lane + off;
+#pragma unroll
+                for (int i = 0; i < kGroup / kRowsAt; ++i) {
+                    const int r = i * kRowsAt;                 // lrow | r: they share no bits
+                    cp16((dst ^ ((r & 7) << 4)) + r * kRowBytes, ks + r * kRowBytes, stream);
+                }
 #pragma unroll
                 for (int i = 0; i < kGroup / kRowsAt; ++i) {
                     const int r = i * kRowsAt;
-                    // chunk ^ (row & 7), row = lrow + r: lrow < kRowsAt and r a multiple of kRowsAt
-                    const uint32_t off = r * kRowBytes + ((chunk ^ (lrow & 7) ^ (r & 7)) << 4);
+                    cp16((dst ^ ((r & 7) << 4)) + r * kRowBytes + S::kHalf, vs + r * kRowBytes, stream);
+                }
+            } else if (valid > 0) {                            // zeros for the rows that are not there
+#pragma unroll 1
+                for (int r = 0; r < kGroup; r += kRowsAt) {
                     const bool in = lrow + r < valid;
-                    const size_t step = in ? (size_t)r * kRowBytes : 0;
-                    cp16(dst + off, in ? ks + step : (const uint8_t*)a.k, in ? 16 : 0);
-                    cp16(dst + off + S::kHalf, in ? vs + step : (const uint8_t*)a.v, in ? 16 : 0);
+                    const size_t from = in ? off + (size_t)r * kRowBytes : 0;
+                    const uint32_t to = (dst ^ ((r & 7) << 4)) + r * kRowBytes;
+                    cp16_or_zero(to, (in ? k_lane : (const uint8_t*)a.k) + from, in);
+                    cp16_or_zero(to + S::kHalf, (in ? v_lane : (const uint8_t*)a.v) + from, in);
                 }
             }
+            fill = fill == kStages - 1 ? 0 : fill + 1;
             ++issued;
             if (issued < steps) {
-                const int u = w.head * a.ng + w.sub;
+                const int head = w.head, sub = w.sub;
                 w.next(a.c, a.ng);
-                fresh = w.head * a.ng + w.sub != u;
+                fresh = w.head != head || w.sub != sub;
                 if (fresh) begins = true;
-                page = page_of();
+                if (fresh || w.tile - page_base >= 32) load_pages();
             }
         }
         cp_commit();
@@ -389,24 +419,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
 
     // ---- the consuming side
     constexpr int kNt = D / 8;                // 8-column tiles of the output
+    constexpr int kR = kWide ? 2 : 1;         // rows of the MMA that are query heads: gid, gid + 8
     float o[kNt][4];
-    float m_run[2], l_run[2];                 // of rows gid and gid + 8 (the latter: kWide only)
+    float m_run[2], l_run[2];                 // running maximum (log2 units) and sum
     uint32_t qf[D / 16][kWide ? 4 : 2];
-    const int b_row = (lane & 7) + ((lane >> 4) & 1) * 8, b_chunk = (lane >> 3) & 1;   // keys
-    const int v_row = (lane & 7) + ((lane >> 3) & 1) * 8, v_chunk = (lane >> 4) & 1;   // values
+    // a lane's address for ldmatrix within a stage: chunk c of its row lies 16 c bytes on, by xor
+    const int k_row = (lane & 7) + ((lane >> 4) & 1) * 8, v_row = (lane & 7) + ((lane >> 3) & 1) * 8;
+    const uint32_t k_at = my_ring + k_row * kRowBytes + ((((lane >> 3) & 1) ^ (k_row & 7)) << 4);
+    const uint32_t v_at = my_ring + S::kHalf + v_row * kRowBytes + ((((lane >> 4) & 1) ^ (v_row & 7)) << 4);
     int segment = 0, seg_step = 0;            // units begun before this one; the step that began it
+    int head = 0, g0 = 0, nq = 0;             // the unit's head, first query head and how many
+    float* lp = nullptr;                      // logits of query head gid, row 2 tig of the head
+    const size_t lp_row = (size_t)a.c.cap();
 
+    int stage = 0;
     for (int step = 0; step < steps; ++step) {
-        const int stage = step % kStages;
         cp_wait<kStages - 2>();
         __syncwarp();
         const Meta m = meta[warp][stage];
         issue();                              // into the stage consumed one step ago
-        const uint32_t sk = my_ring + stage * S::kStage, sv = sk + S::kHalf;
-        const int head = m.unit / a.ng, g0 = (m.unit - head * a.ng) * a.gq;
-        const int nq = min(a.gq, a.G - g0);   // query heads of this unit
-        if (m.flags & kFirst) {
+        const int valid = m.valid_flags & kValid;
+        if (m.valid_flags & kFirst) {
             seg_step = step;
+            head = m.head;
+            g0 = m.sub * a.gq;
+            nq = min(a.gq, a.G - g0);
 #pragma unroll
             for (int i = 0; i < kNt; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
             m_run[0] = m_run[1] = kLowest;
@@ -422,44 +459,49 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
                     qf[ks][3] = gid + 8 < nq ? qp[(gid + 8) * (D / 2) + at32 + 4] : 0u;
                 }
             }
+            lp = a.logits + ((size_t)head * a.G + g0 + gid) * lp_row + 2 * tig;
         }
-        if (m.valid > 0) {
+        if (valid > 0) {
             // logits of 16 rows: two tiles of 8 rows, two chains each
             float c[2][2][4] = {};
+            const uint32_t sk = k_at + stage * S::kStage, sv = v_at + stage * S::kStage;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 uint32_t b0, b1, b2, b3;
-                ldsm4(sk + b_row * kRowBytes + (((2 * ks + b_chunk) ^ (b_row & 7)) << 4), b0, b1, b2, b3);
+                ldsm4(sk ^ (ks << 5), b0, b1, b2, b3);
                 const uint32_t a1 = kWide ? qf[ks][kWide ? 2 : 0] : 0u, a3 = kWide ? qf[ks][kWide ? 3 : 0] : 0u;
                 Pair<T>::mma(c[ks & 1][0], qf[ks][0], a1, qf[ks][1], a3, b0, b1);
                 Pair<T>::mma(c[ks & 1][1], qf[ks][0], a1, qf[ks][1], a3, b2, b3);
             }
-            float t[2][4];                    // [8-row tile][row gid: 2 cached rows, row gid + 8: 2]
+            float t[2][2 * kR];               // [8-row tile][query head gid: 2 cached rows, gid + 8: 2]
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = n * 8 + 2 * tig + (i & 1);
-                    t[n][i] = j < m.valid ? (c[0][n][i] + c[1][n][i]) * a.scale2 : -INFINITY;
-                }
-            if (a.logits) {
-                float* lp = a.logits + ((size_t)head * a.G + g0) * a.c.cap() + m.row0 + 2 * tig;
+                for (int i = 0; i < 2 * kR; ++i) t[n][i] = c[0][n][i] + c[1][n][i];
+            if (valid < kGroup) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    if (gid < nq) *(float2*)(lp + (size_t)gid * a.c.cap() + n * 8) = make_float2(t[n][0], t[n][1]);
-                    if (kWide && gid + 8 < nq)
-                        *(float2*)(lp + (size_t)(gid + 8) * a.c.cap() + n * 8) = make_float2(t[n][2], t[n][3]);
-                }
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2 * kR; ++i)
+                        if (n * 8 + 2 * tig + (i & 1) >= valid) t[n][i] = -INFINITY;
+            }
+            if (a.logits) {
+#pragma unroll
+                for (int r = 0; r < kR; ++r)
+                    if (gid + 8 * r < nq) {
+                        float* to = lp + m.row0 + r * 8 * lp_row;
+                        *(float2*)to = make_float2(t[0][2 * r], t[0][2 * r + 1]);
+                        *(float2*)(to + 8) = make_float2(t[1][2 * r], t[1][2 * r + 1]);
+                    }
             }
             uint32_t pa[4];                   // the weights as the A operand of P V
 #pragma unroll
-            for (int r = 0; r < (kWide ? 2 : 1); ++r) {
+            for (int r = 0; r < kR; ++r) {
                 float mx = fmaxf(fmaxf(t[0][2 * r], t[0][2 * r + 1]), fmaxf(t[1][2 * r], t[1][2 * r + 1]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float m_new = fmaxf(m_run[r], mx);
-                if (__any_sync(0xffffffffu, m_new > m_run[r])) {
-                    const float f = ptx::ex2(m_run[r] - m_new);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * a.scale2;
+                if (__any_sync(0xffffffffu, mx > m_run[r])) {
+                    const float m_new = fmaxf(m_run[r], mx), f = ptx::ex2(m_run[r] - m_new);
                     l_run[r] *= f;
 #pragma unroll
                     for (int i = 0; i < kNt; ++i) {
@@ -473,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
                     m_run[r] = m_new;
                 }
                 const float off = Pair<T>::kBias - m_run[r];
-                const float p0 = ptx::ex2(t[0][2 * r] + off), p1 = ptx::ex2(t[0][2 * r + 1] + off);
-                const float p2 = ptx::ex2(t[1][2 * r] + off), p3 = ptx::ex2(t[1][2 * r + 1] + off);
+                const float p0 = ptx::ex2(fmaf(t[0][2 * r], a.scale2, off)), p1 = ptx::ex2(fmaf(t[0][2 * r + 1], a.scale2, off));
+                const float p2 = ptx::ex2(fmaf(t[1][2 * r], a.scale2, off)), p3 = ptx::ex2(fmaf(t[1][2 * r + 1], a.scale2, off));
                 l_run[r] += (p0 + p1) + (p2 + p3);
                 pa[r] = Pair<T>::pack(p0, p1);
                 pa[r + 2] = Pair<T>::pack(p2, p3);
@@ -487,12 +529,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
 #pragma unroll
             for (int i = 0; i < kNt; i += 2) {
                 uint32_t b0, b1, b2, b3;
-                ldsm4t(sv + v_row * kRowBytes + (((i + v_chunk) ^ (v_row & 7)) << 4), b0, b1, b2, b3);
+                ldsm4t(sv ^ (i << 4), b0, b1, b2, b3);
                 Pair<T>::mma(o[i], pa[0], pa[1], pa[2], pa[3], b0, b1);
                 Pair<T>::mma(o[i + 1], pa[0], pa[1], pa[2], pa[3], b2, b3);
             }
         }
-        if (m.flags & kLast) {
+        if (m.valid_flags & kLast) {
             // ---- join the four warps' parts, each in the stage it has just consumed
             __syncwarp();
             float* part = (float*)(ring + (size_t)(warp * kStages + stage) * S::kStage);
@@ -512,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
             }
             __syncthreads();
             const int slot = 2 * cta + (segment ? 1 : 0);
-            const bool whole = m.flags & kWhole;
+            const bool whole = m.valid_flags & kWhole;
             for (int e = tid; e < nq * D; e += kThreads) {
                 const int row = e / D, col = e % D;
                 float top = kLowest;
@@ -545,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
             if (!whole && tid == 0) {
                 Cut x;
                 const int tile = m.row0 / kTile - (step - seg_step);   // the share's first
-                x.unit = m.unit;
+                x.unit = head * a.ng + m.sub;
                 x.head = head;
                 x.tile = tile;
                 x.count = step - seg_step + 1;
@@ -561,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
                 add_weights<kThreads>(a, head, 0, a.c.len(head), tid, sh_lse2);
             segment = 1;
         }
+        stage = stage == kStages - 1 ? 0 : stage + 1;
     }
 }
 
