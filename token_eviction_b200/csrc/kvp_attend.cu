@@ -23,6 +23,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kvp_cache.cuh"
 #include "kvp_ptx.cuh"
@@ -36,8 +37,8 @@ constexpr int kGroup = 16;                        // rows a warp takes at a time
 constexpr int kTile = kWarps * kGroup;            // rows a CTA takes at a time
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxGrid = kPlanGrid * kCtasPerSm;  // the workspace holds parts for as many CTAs
-constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinPieces = 4;                    // blocks of attend_join that share one part
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinPieces = 4;                    // blocks of attend_join that weigh one share
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.4028234663852886e38f;  // of a maximum over nothing: finite, so that
                                                     // differences of maxima are never inf - inf
@@ -607,91 +608,104 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
     }
 }
 
-// log2 of the sum of a unit's parts over query head `row`, by one warp.
-__device__ __forceinline__ float joined_lse2(const AttendArgs& a, const Cut& p, int row) {
+// A warp's sum over the parts of a unit for query head `row`: log2 of it, and (mine) the maximum
+// of part `lane`.
+__device__ __forceinline__ float joined_lse2(const AttendArgs& a, const Cut& p, int row, float& mine) {
     const int lane = threadIdx.x & 31;
-    float top = kLowest;
-    for (int i = lane; i < p.n; i += 32) top = fmaxf(top, a.stats[p.slot(i) * a.gq + row].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float l = 0.f;
-    for (int i = lane; i < p.n; i += 32) {
-        const float2 st = a.stats[p.slot(i) * a.gq + row];
-        l += st.y * ptx::ex2(st.x - top);
+    float2 st = lane < p.n ? a.stats[p.slot(lane) * a.gq + row] : make_float2(kLowest, 0.f);
+    mine = st.x;
+    float top = st.x, l = st.y;
+    for (int i = lane + 32; i < p.n; i += 32) {
+        st = a.stats[p.slot(i) * a.gq + row];
+        const float m = fmaxf(top, st.x);
+        l = l * ptx::ex2(top - m) + st.y * ptx::ex2(st.x - m);
+        top = m;
     }
+    float m = top;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    l *= ptx::ex2(top - m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    return top + log2f(l);
+    return m + log2f(l);
 }
 
-// kJoinPieces blocks for each share of a cut unit: its rows' weights go to acc, and the blocks of
-// the unit's first share join its output, a query head each at a time.
+// Two kinds of blocks, none with more than one short chain of reads. The first kJoinPieces blocks
+// for every share of a cut unit (with acc): add its rows' weights. Then `rows` blocks for every CTA
+// of attend_split, one a query head: join the outputs of the units whose first share it had.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendArgs a) {
-    constexpr int kCols = D / 32;             // columns a lane joins
+__global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendArgs a, int weighers, int rows) {
     __shared__ float sh_lse2[16];
-    __shared__ float sh_val[kJoinWarps][D];
     ptx::grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int slot = blockIdx.x / kJoinPieces, piece = blockIdx.x % kJoinPieces;
-    const Cut p = a.cuts[slot];
-    if (p.unit < 0) return;
-    const int g0 = (p.unit - p.head * a.ng) * a.gq, nq = min(a.gq, a.G - g0);
-    const bool weigh = a.logits && a.ng == 1, joins = p.tile == 0;
-    if (weigh || joins) {
-        for (int row = warp; row < nq; row += kJoinWarps) {
-            const float x = joined_lse2(a, p, row);
-            if (lane == 0) sh_lse2[row] = x;
+    if ((int)blockIdx.x < weighers) {
+        const Cut p = a.cuts[blockIdx.x / kJoinPieces];
+        const int piece = blockIdx.x % kJoinPieces;
+        constexpr int kRound = kJoinThreads * 4;
+        const int last = min(p.len, (p.tile + p.count) * kTile), first = p.tile * kTile + piece * kRound;
+        if (p.unit < 0 || first >= last) return;
+        for (int row = warp; row < a.G; row += kJoinWarps) {
+            float mine;
+            const float x = joined_lse2(a, p, row, mine);
+            if (lane == 0) sh_lse2[row] = x == -INFINITY ? INFINITY : x;
         }
-    }
-    __syncthreads();
-    if (joins) {
-        for (int row = piece; row < nq; row += kJoinPieces) {
-            const float x = sh_lse2[row];
-            const size_t query = (size_t)p.head * a.G + g0 + row;
-            float val[kCols] = {};
-            if (x != -INFINITY) {
-#pragma unroll 4
-                for (int i = warp; i < p.n; i += kJoinWarps) {
-                    const size_t s = p.slot(i) * a.gq + row;
-                    const float f = ptx::ex2(a.stats[s].x - x);
-                    const float* from = a.parts + s * D + lane * kCols;
-                    if constexpr (kCols == 4) {
-                        const float4 y = *(const float4*)from;
-                        val[0] += f * y.x;
-                        val[1] += f * y.y;
-                        val[2] += f * y.z;
-                        val[3] += f * y.w;
-                    } else {
-                        const float2 y = *(const float2*)from;
-                        val[0] += f * y.x;
-                        val[1] += f * y.y;
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) sh_val[warp][lane * kCols + i] = val[i];
-            __syncthreads();
-            if (tid < D) {
-                float sum = 0.f;
-#pragma unroll
-                for (int y = 0; y < kJoinWarps; ++y) sum += sh_val[y][tid];
-                ((T*)a.out)[query * D + tid] = T(sum);
-                if (tid == 0) {
-                    if (a.lse) a.lse[query] = x * kLn2;
-                    if (a.lse2) a.lse2[query] = x;
-                }
-            }
-            __syncthreads();
-        }
-    }
-    if (weigh) {
-        if (tid < nq && sh_lse2[tid] == -INFINITY) sh_lse2[tid] = INFINITY;
         __syncthreads();
-        // rows of this share, dealt to its blocks kJoinThreads * 4 at a time
-        const int last = min(p.len, (p.tile + p.count) * kTile);
-        for (int j = p.tile * kTile + piece * kJoinThreads * 4; j < last; j += kJoinPieces * kJoinThreads * 4)
-            add_weights<kJoinThreads>(a, p.head, j, min(last, j + kJoinThreads * 4), tid, sh_lse2);
+        for (int j = first; j < last; j += kJoinPieces * kRound)
+            add_weights<kJoinThreads>(a, p.head, j, min(last, j + kRound), tid, sh_lse2);
+        return;
+    }
+    // a warp every kJoinWarps-th part, kAhead of them read before their sum is known; a lane kCols columns
+    constexpr int kCols = D / 32, kAhead = 32 / kJoinWarps;
+    using Piece = typename std::conditional<kCols == 4, float4, float2>::type;
+    __shared__ float sh_val[kJoinWarps][D];
+    const int cta = (blockIdx.x - weighers) / rows, row = (blockIdx.x - weighers) % rows;
+    for (int s = 0; s < 2; ++s) {
+        const Cut p = a.cuts[2 * cta + s];
+        if (p.unit < 0 || p.tile != 0) continue;
+        const int g0 = (p.unit - p.head * a.ng) * a.gq;
+        if (g0 + row >= a.G) continue;
+        Piece y[kAhead];
+        auto read = [&](int base) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int part = base + i * kJoinWarps + warp;
+                if (part < p.n) y[i] = ((const Piece*)(a.parts + (p.slot(part) * a.gq + row) * D))[lane];
+            }
+        };
+        read(0);
+        float mine;
+        const float lse2 = joined_lse2(a, p, row, mine);
+        const size_t query = (size_t)p.head * a.G + g0 + row;
+        float val[kCols] = {};
+        for (int base = 0; base < p.n; base += 32) {
+            if (base > 0) {
+                read(base);
+                mine = base + lane < p.n ? a.stats[p.slot(base + lane) * a.gq + row].x : kLowest;
+            }
+            const float f = lse2 == -INFINITY ? 0.f : ptx::ex2(mine - lse2);  // of part base + lane
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int part = i * kJoinWarps + warp;
+                const float fi = __shfl_sync(0xffffffffu, f, part);
+                if (base + part >= p.n) continue;
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) val[c] += fi * ((const float*)&y[i])[c];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) sh_val[warp][lane * kCols + c] = val[c];
+        __syncthreads();
+        if (tid < D) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) sum += sh_val[w][tid];
+            ((T*)a.out)[query * D + tid] = T(sum);
+        }
+        if (tid == 0) {
+            if (a.lse) a.lse[query] = lse2 * kLn2;
+            if (a.lse2) a.lse2[query] = lse2;
+        }
+        __syncthreads();
     }
 }
 
@@ -759,7 +773,8 @@ cudaError_t launch_all(const AttendArgs& a, int grid, cudaStream_t st) {
     cudaError_t e = a.gq == 16 ? launch_split<T, D, true, kStages>(a, grid, st)
                                      : launch_split<T, D, false, kStages>(a, grid, st);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(attend_join<T, D>, 2 * grid * kJoinPieces, kJoinThreads, 0, st, a);
+    const int weighers = a.logits && a.ng == 1 ? 2 * grid * kJoinPieces : 0, rows = std::min(a.G, a.gq);
+    e = launch_dependent(attend_join<T, D>, weighers + grid * rows, kJoinThreads, 0, st, a, weighers, rows);
     if (e != cudaSuccess || !a.lse2) return e;
     const int per = std::max(1, std::min(num_sms() * 8 / a.c.heads, (a.c.cap() + kJoinThreads * 4 - 1) / (kJoinThreads * 4)));
     return launch_dependent(attend_weigh, a.c.heads * per, kJoinThreads, 0, st, a, per);
