@@ -1,7 +1,8 @@
 """Prefill KV-cache token eviction (S1 * S2 scores) on NVIDIA B200: Python binding.
 
-A thin ctypes layer over the C-ABI library ``libkvp.so`` (declared in
-``include/kvp.h``). It only marshals arguments: every step of the path - the split-L
+A thin layer over the C-ABI library ``libkvp.so`` (declared in ``include/kvp.h``): ctypes, and
+for the paged cache's calls, which a decode makes for every token, ``_kvp_binding.so``. It only
+marshals arguments: every step of the path - the split-L
 log-sum-exp pass, the scoring pass, the selection and the compaction - runs in the
 library's CUDA kernels. PyTorch provides device memory and streams.
 
@@ -28,8 +29,8 @@ plus ``evict_layer``, which allocates the outputs and runs the first three calls
 ``LayerCache``, the paged cache that a decode reads: it takes what ``evict_layer`` kept, appends
 and attends token by token, and keeps to a budget.
 
-There is no fallback: if ``libkvp.so`` is missing or cannot be loaded, importing this
-package raises.
+There is no fallback: if ``libkvp.so`` or ``_kvp_binding.so`` is missing or cannot be loaded,
+importing this package raises.
 """
 from __future__ import annotations
 
@@ -160,6 +161,13 @@ def _load():
 
 
 _lib = _load()
+try:
+    from . import _kvp_binding
+except ImportError as e:
+    raise ImportError(f"_kvp_binding.so cannot be loaded ({e}): build it with "
+                      "`python token_eviction_b200/build.py` (there is no fallback implementation)") from e
+_kvp_binding.use(*(ctypes.cast(f, ctypes.c_void_p).value
+                   for f in (_lib.kvp_cache_append, _lib.kvp_cache_attend, _lib.kvp_cache_evict)))
 
 # Kernel launches one layer's kvp_score + kvp_select + kvp_compact makes: the fused
 # scoring kernel (both passes over K), the selection and the gather. kvp_score also
@@ -388,36 +396,17 @@ def evict_layer(q_win, k, v, window: int, budget: int, buffers: LayerBuffers | N
 # ---- the paged cache
 
 
-def _cache_args(items):
-    """Pointers of `items`, (tensor or None, name, dtype, shape) each: CUDA tensors on one device,
-    contiguous, of that type and shape. Returns the pointers and the device's index."""
-    ptrs, dev = [], None
-    for t, name, dtype, shape in items:
-        if t is None:
-            ptrs.append(None)
-            continue
-        ptrs.append(_ptr(t, name, dtype, shape))
-        if dev is None:
-            dev = t.device.index
-        elif t.device.index != dev:
-            raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{dev}")
-    return ptrs, dev
-
-
-def _on(dev, call, *args, stream=None):
-    """call(*args, stream) with the tensors' device current, on `stream` (by default that device's
-    current one): streams and launches belong to a device."""
-    if dev == torch.cuda.current_device():
-        return call(*args, _stream(stream))
-    with torch.cuda.device(dev):
-        return call(*args, _stream(stream))
-
-
 def _kept_for(stream, workspace):
     """A workspace that the call made itself lives until `stream` is done with it."""
     if stream is not None:
         workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
                                 else torch.cuda.ExternalStream(int(stream), device=workspace.device))
+
+
+def _device_of(t):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("a paged cache's tensors must be CUDA tensors")
+    return t.device
 
 
 def _cache_workspace(nbytes, what, device):
@@ -436,49 +425,13 @@ def evict_workspace_for(shape, evict, device=None) -> torch.Tensor:
     return _cache_workspace(n, "kvp_cache_evict_workspace_bytes", device)
 
 
-def _pool(sh, k_pages, v_pages, table, lens, dt):
-    pool, heads = (sh.num_pages, sh.page_size, sh.head_dim), (sh.batch, sh.hkv)
-    return [(k_pages, "k_pages", dt, pool), (v_pages, "v_pages", dt, pool),
-            (table, "table", torch.int32, heads + (sh.max_pages,)), (lens, "lens", torch.int32, heads)]
-
-
-def _dtype(sh):
-    if not 0 <= sh.dtype < len(_DTYPES):
-        raise KvpError(2, "kvp_cache_shape")
-    return _DTYPES[sh.dtype]
-
-
-def _required(**tensors):
-    for name, t in tensors.items():
-        if t is None:
-            raise ValueError(f"{name} is required")
-
-
 def kvp_cache_append(shape, k_new, v_new, k_pages, v_pages, table, lens, lens_out, acc=None, weight=None,
                      counts=None, stream=None):
     """Appends n rows per head: k_new and v_new [b, hkv, n, d], or packed head after head
     [b, hkv * n, d] with counts [b, hkv]. weight: the rows' first accumulated weights, shaped
     like k_new without its last dimension. lens_out may be lens."""
-    sh = shape
-    _required(k_new=k_new, v_new=v_new, k_pages=k_pages, v_pages=v_pages, table=table, lens=lens,
-              lens_out=lens_out)
-    dt, b, hkv = _dtype(sh), sh.batch, sh.hkv
-    if counts is None:
-        n = k_new.shape[2] if k_new.dim() == 4 else -1
-        rows = (b, hkv, n)
-    else:
-        n = k_new.shape[1] // hkv if k_new.dim() == 3 else -1
-        rows = (b, hkv * n)
-    if n < 0:
-        raise ValueError("k_new must be [b, hkv, n, d], or [b, hkv * n, d] with counts")
-    (k, v, kp, vp, pt, pl, plo, pa, pw, pc), dev = _cache_args(
-        [(k_new, "k_new", dt, rows + (sh.head_dim,)), (v_new, "v_new", dt, rows + (sh.head_dim,))]
-        + _pool(sh, k_pages, v_pages, table, lens, dt)
-        + [(lens_out, "lens_out", torch.int32, (b, hkv)),
-           (acc, "acc", torch.float32, (sh.num_pages, sh.page_size)),
-           (weight, "weight", torch.float32, rows), (counts, "counts", torch.int32, (b, hkv))])
-    st = _on(dev, _lib.kvp_cache_append, ctypes.byref(sh), k, v, n, pc, pw, kp, vp, pa, pt, pl, plo,
-             stream=stream)
+    st = _kvp_binding.append(shape, k_new, v_new, k_pages, v_pages, table, lens, lens_out, acc, weight, counts,
+                             stream)
     if st != KVP_OK:
         raise KvpError(st, "kvp_cache_append")
 
@@ -486,19 +439,10 @@ def kvp_cache_append(shape, k_new, v_new, k_pages, v_pages, table, lens, lens_ou
 def kvp_cache_attend(shape, q, k_pages, v_pages, table, lens, out, lse=None, acc=None, workspace=None,
                      stream=None):
     """Attention of one token q [b, hq, d] over the cache; acc gains each row's weights."""
-    sh = shape
-    _required(q=q, k_pages=k_pages, v_pages=v_pages, table=table, lens=lens, out=out)
-    dt, heads = _dtype(sh), (sh.batch, sh.hq)
     own = workspace is None
     if own:
-        workspace = attend_workspace_for(sh, acc is not None, q.device)
-    (kp, vp, pt, pl, pq, po, ps, pa, pw), dev = _cache_args(
-        _pool(sh, k_pages, v_pages, table, lens, dt)
-        + [(q, "q", dt, heads + (sh.head_dim,)), (out, "out", dt, heads + (sh.head_dim,)),
-           (lse, "lse", torch.float32, heads), (acc, "acc", torch.float32, (sh.num_pages, sh.page_size)),
-           (workspace, "workspace", torch.uint8, None)])
-    st = _on(dev, _lib.kvp_cache_attend, ctypes.byref(sh), pq, kp, vp, pt, pl, po, ps, pa, pw,
-             workspace.numel(), stream=stream)
+        workspace = attend_workspace_for(shape, acc is not None, _device_of(q))
+    st = _kvp_binding.attend(shape, q, k_pages, v_pages, table, lens, out, lse, acc, workspace, stream)
     if own:
         _kept_for(stream, workspace)
     if st != KVP_OK:
@@ -510,21 +454,12 @@ def kvp_cache_evict(shape, evict, k_pages, v_pages, acc, acc_out, table, lens, l
     """Each head keeps its first `sinks` rows, its last `window` and the heaviest between them, up to
     its budget (a KvpEvict, or a dict of make_evict's arguments). In place; acc_out may be acc
     and lens_out lens."""
-    sh = shape
-    ev = evict if isinstance(evict, KvpEvict) else make_evict(**evict)
-    _required(k_pages=k_pages, v_pages=v_pages, acc=acc, acc_out=acc_out, table=table, lens=lens,
-              lens_out=lens_out)
-    dt, heads, pool = _dtype(sh), (sh.batch, sh.hkv), (sh.num_pages, sh.page_size)
+    ev = make_evict(**evict) if isinstance(evict, dict) else evict
     own = workspace is None
     if own:
-        workspace = evict_workspace_for(sh, ev, acc.device)
-    (kp, vp, pt, pl, pa, pao, plo, ps, pb, pw), dev = _cache_args(
-        _pool(sh, k_pages, v_pages, table, lens, dt)
-        + [(acc, "acc", torch.float32, pool), (acc_out, "acc_out", torch.float32, pool),
-           (lens_out, "lens_out", torch.int32, heads), (src, "src", torch.int32, heads + (ev.budget,)),
-           (budgets, "budgets", torch.int32, heads), (workspace, "workspace", torch.uint8, None)])
-    st = _on(dev, _lib.kvp_cache_evict, ctypes.byref(sh), ctypes.byref(ev), pb, kp, vp, pa, pao, pt, pl, plo,
-             ps, pw, workspace.numel(), stream=stream)
+        workspace = evict_workspace_for(shape, ev, _device_of(k_pages))
+    st = _kvp_binding.evict(shape, ev, k_pages, v_pages, acc, acc_out, table, lens, lens_out, src, budgets,
+                            workspace, stream)
     if own:
         _kept_for(stream, workspace)
     if st != KVP_OK:

@@ -4,7 +4,8 @@
 
 (Run it as a script: importing the package loads the library this builds.)
 
-The library is plain C ABI over CUDA: every ``csrc/*.cu`` is compiled for
+``_kvp_binding.so`` beside it is the Python entry of the calls that a decode makes (g++ against
+torch's and Python's headers). The library is plain C ABI over CUDA: every ``csrc/*.cu`` is compiled for
 ``sm_100a`` and linked into one shared object beside this file, with the CUDA runtime
 linked statically. The driver API entry points it needs are fetched at run time.
 """
@@ -104,7 +105,36 @@ def build_checks(force: bool = False, verbose: bool = False) -> str:
     return build(force=True, verbose=verbose, out=CHECKS_LIB, defines=("KVP_CHECKS",))
 
 
+# The Python entry of the paged-cache calls.
+BINDING = os.path.join(PKG, "_kvp_binding.so")
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    src = os.path.join(CSRC, "kvp_binding.cpp")
+    deps = [src, os.path.join(INCLUDE, "kvp.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in deps):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+           *[x for d in cpp_extension.include_paths() for x in ("-isystem", d)], src, "-o", tmp,
+           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 if __name__ == "__main__":
+    build_binding(force="--force" in sys.argv, verbose="-v" in sys.argv)
     build(force="--force" in sys.argv, verbose="-v" in sys.argv)
     print(LIB)
     if "--checks" in sys.argv:
