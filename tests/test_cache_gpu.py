@@ -159,10 +159,12 @@ def test_evict_edges(page, budget, sinks, window, lens, in_place):
 @pytest.mark.parametrize("b,hkv,rows,budget,spread", [(1, 8, 32768, 2048, False), (1, 2, 32768, 22937, False),
                                                       (64, 8, 2064, 2048, True), (1, 1, 131072, 91750, False),
                                                       (1, 1, 450000, 1000, False), (2, 2, 9000, 8999, True),
-                                                      (160, 1, 8000, 4000, True)])
+                                                      (160, 1, 8000, 4000, True), (1, 1, 200000, 60000, False),
+                                                      (80, 1, 16384, 5000, True), (1, 8, 4200, 4100, False),
+                                                      (100, 2, 900, 700, True), (3, 1, 65536, 300, True)])
 def test_evict_sizes(b, hkv, rows, budget, spread):
-    """The sizes that select each variant: one CTA or a cluster a head, keys in shared memory or read
-    again from the cache."""
+    """The sizes that select each variant: one CTA or a cluster a head, keys in registers, in shared
+    memory or read again from the cache."""
     over = rows - budget
     lens = [budget + (over * i // max(1, b * hkv - 1) if spread else over) for i in range(b * hkv)]
     c = Cache(rows, b, hkv, hkv, 64, 64, lens)

@@ -1,17 +1,24 @@
 // Eviction from a paged cache by accumulated attention weight, in place.
 //
-// evict_select: a cluster of C CTAs per head. Each CTA holds the keys of a slice of the head's
-// rows in shared memory: a weight's bits, which order as the weights do (all are non-negative
-// or count as zero). A radix select, four bits a round from the top, finds the key T of the
-// last row that stays: every thread counts its keys' digits in 16 packed byte counters, warps
-// add them by redux, CTAs exchange 16 sums each, and every warp of every CTA finds the same
-// digit, so a round costs one block barrier and (C > 1) one cluster barrier; no atomics, whatever
-// the distribution. It stops early once all keys that share the prefix stay. The rows that
-// change places are then listed, in row order, by counts exchanged once: the evicted places below
-// t - w and the kept rows at or past it.
-// evict_move: copies the listed rows (keys, values, weight), then the window. Only rows in
-// [t - w, t) are both a source and a place to write to: the kept rows there are the first of
-// the list, and the block that copies them copies the window after them.
+// A head's rows are ranked by their weights' bits, which order as the weights do (all are
+// non-negative or count as zero); T, the key of the last row that stays, is found by its bits from
+// the top, and the rows that change places are listed in row order: the evicted places below
+// t - w and the kept rows at or past it. Those are copied (keys, values, weight), then the window.
+// Nothing else moves: a head that gives up e of its rows copies at most e + w.
+//
+// evict_select (up to 16 K rows a CTA): one CTA, or a cluster of 8, per head, each thread holding the
+// keys of kPer consecutive rows in registers. Eight bits of T a round, by a histogram in shared
+// memory; a cluster's CTAs write theirs into one another's shared memory. Every warp finds the
+// digit by itself, so that a round has one barrier (and one of the cluster). It ends as soon as
+// all keys that share T's bits stay. One scan of packed counts then gives every thread its places
+// in the lists. A head with few rows to copy is finished here.
+// (Two bits a round by counting keys against three candidates, with no atomics: 28 us where this
+// takes 17 for 512 heads of 2064 rows.)
+// evict_select_long: longer rows, keys in shared memory or read again each round, four bits a round by
+// packed counters.
+// evict_move: copies the listed rows of the other heads. Only rows in [t - w, t) are both a source and
+// a place to write to: the kept rows there are the first of the list, and the block that copies
+// them copies the window after them.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -26,8 +33,12 @@ namespace {
 
 constexpr int kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kSliceCap = 48 * 1024;     // keys a CTA holds in shared memory
-constexpr int kMoveThreads = 256, kMoveRows = 4;
+constexpr int kSliceCap = 48 * 1024;     // keys a CTA of evict_select_long holds in shared memory
+constexpr int kPerMost = 16;             // keys a thread of evict_select holds
+constexpr int kMoveThreads = 256;
+constexpr int kMoveLoads = 8;            // 16-byte loads a lane has in flight in evict_move,
+constexpr int kFewLoads = 4;             // and in evict_select, whose threads may have 64 registers
+constexpr int kFew = 256;                // rows that evict_select copies itself (one CTA a head)
 
 struct EvictArgs {
     CacheView c;
@@ -40,10 +51,10 @@ struct EvictArgs {
     int32_t* src;             // NULL: not wanted
     int B, s, w;
     // workspace
-    int4* info;               // [heads]: n, t, rows listed, -
+    int4* info;               // [heads]: n, t, rows listed, whether they are still to be copied
     int32_t* from;            // [heads][B]: listed rows, ascending
     int32_t* to;              // [heads][B]: the places they move to, ascending
-    int slice;                // keys that shared memory holds per CTA; 0: keys are read from acc again and again
+    int slice;                // evict_select_long: keys that shared memory holds per CTA; 0: read again each round
 };
 
 __device__ __forceinline__ uint32_t key_of(float weight) {
@@ -69,7 +80,7 @@ __device__ __forceinline__ void sync_all() {
 }
 
 template <int C>
-__global__ void __launch_bounds__(kMaxThreads, 1) evict_select(const EvictArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 1) evict_select_long(const EvictArgs a) {
     extern __shared__ __align__(16) uint32_t keys[];
     __shared__ SelectShared sh;
     ptx::grid_dependency_wait();
@@ -244,7 +255,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) evict_select(const EvictArgs a
             kept_low = l0;
             kept_high = h0;
             if (lane == 0) {
-                a.info[head] = make_int4(n, t, listed, 0);
+                a.info[head] = make_int4(n, t, listed, 1);
                 a.lens_out[head] = t;                 // every CTA has read lens
             }
         }
@@ -281,52 +292,66 @@ __global__ void __launch_bounds__(kMaxThreads, 1) evict_select(const EvictArgs a
     if (C > 1) cg::this_cluster().sync();             // shared memory outlives its readers
 }
 
-// Rows `from` -> `to` of a head, kMoveRows at a time per group of lanes; all rows of a round are
-// read before any is written (by every thread of the block when kBarrier).
-template <int D, bool kBarrier, typename Pair>
-__device__ __forceinline__ void move_rows(const EvictArgs& a, int head, int first, int last, int stride, Pair pair) {
-    constexpr int kPieces = D / 8, kLanes = 2 * kPieces, kGroups = kMoveThreads / kLanes;
-    const int lane = threadIdx.x % kLanes, piece = lane % kPieces, group = threadIdx.x / kLanes;
-    uint4* pool = lane >= kPieces ? a.v_pages : a.k_pages;
-    for (int base = first; base < last; base += stride) {
-        uint4 x[kMoveRows];
-        float wt[kMoveRows];
-        long long dst[kMoveRows];
-#pragma unroll
-        for (int r = 0; r < kMoveRows; ++r) {
-            dst[r] = -1;
-            const int i = base + r * kGroups + group;
-            if (i >= last) continue;
-            const int2 p = pair(i);
-            const long long from = a.c.row(head, p.x), to = a.c.row(head, p.y);
-            if (a.src && lane == 0) a.src[(size_t)head * a.B + p.y] = p.x;
-            if (from < 0 || to < 0) continue;
-            dst[r] = to;
-            x[r] = pool[from * kPieces + piece];
-            if (lane == 0) wt[r] = a.acc[from];
+// Copies rows pair(i) = (source, place) of a head, i in [first, last), `chunk` (up to 32) at a time by
+// each warp: a lane looks up one row's pages and copies its weight; then the warp copies the
+// rows, kLoads loads in flight. kBarrier: all rows of a round (kLoads loads a warp) are read by
+// every thread of the block before any is written.
+template <int D, int kLoads, bool kBarrier, typename PairOf>
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int head, int first, int last, int stride, int chunk,
+                                          int warp, PairOf pair) {
+    constexpr int kPieces = D / 8, kLanes = 2 * kPieces, kAtOnce = 32 / kLanes;   // rows a load instruction covers
+    constexpr int kBatch = kLoads * kAtOnce;
+    const int lane = threadIdx.x & 31, piece = lane % kPieces, sub = lane / kLanes;
+    uint4* pool = (lane / kPieces) & 1 ? a.v_pages : a.k_pages;
+    for (int round = first; round < last; round += stride) {
+        const int base = round + warp * chunk, here = min(chunk, last - base);   // rows of this warp (may be < 1)
+        long long from = -1, to = -1;
+        float weight = 0.f;
+        if (lane < here) {
+            const int2 p = pair(base + lane);
+            from = a.c.row(head, p.x);
+            to = a.c.row(head, p.y);
+            if (a.src) a.src[(size_t)head * a.B + p.y] = p.x;
+            if (from < 0 || !KVP_CHECK(to < ((long long)a.c.num_pages << a.c.page_shift), 703, head, p.y)) to = -1;
+            if (to >= 0) weight = a.acc[from];
         }
-        if (kBarrier) __syncthreads();
+        if (!kBarrier && to >= 0) a.acc_out[to] = weight;
+        for (int i0 = 0; i0 < (kBarrier ? kBatch : here); i0 += kBatch) {
+            uint4 x[kLoads];
+            long long at[kLoads];
 #pragma unroll
-        for (int r = 0; r < kMoveRows; ++r) {
-            if (dst[r] < 0) continue;
-            if (!KVP_CHECK(dst[r] < ((long long)a.c.num_pages << a.c.page_shift), 703, head, base)) continue;
-            pool[dst[r] * kPieces + piece] = x[r];
-            if (lane == 0) a.acc_out[dst[r]] = wt[r];
+            for (int r = 0; r < kLoads; ++r) {
+                const int i = i0 + r * kAtOnce + sub;
+                const long long f = __shfl_sync(0xffffffffu, from, i & 31);
+                at[r] = __shfl_sync(0xffffffffu, to, i & 31);
+                if (i >= here) at[r] = -1;
+                if (at[r] >= 0) x[r] = pool[f * kPieces + piece];
+            }
+            if (kBarrier) __syncthreads();
+#pragma unroll
+            for (int r = 0; r < kLoads; ++r)
+                if (at[r] >= 0) pool[at[r] * kPieces + piece] = x[r];
+            if (kBarrier && to >= 0) a.acc_out[to] = weight;
         }
         if (kBarrier) __syncthreads();
     }
+}
+// Rows that a warp's kLoads loads cover.
+template <int D>
+__host__ __device__ constexpr int batch_rows(int loads) {
+    return loads * (32 / (D / 4));
 }
 
 // parts blocks per head: the listed rows that lie past t are dealt over all of them; block 0 first
 // copies those below t, then the window.
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) evict_move(const EvictArgs a, int parts) {
-    constexpr int kRound = kMoveThreads / (D / 4) * kMoveRows;
+__global__ void __launch_bounds__(kMoveThreads) evict_move(const EvictArgs a, int parts, int chunk) {
+    constexpr int kWarps = kMoveThreads / 32, kBatch = batch_rows<D>(kMoveLoads);
     ptx::grid_dependency_wait();
-    const int head = blockIdx.x / parts, part = blockIdx.x % parts;
+    const int head = blockIdx.x / parts, part = blockIdx.x % parts, warp = threadIdx.x >> 5;
     const int4 info = a.info[head];
-    const int n = info.x, t = info.y, listed = info.z, w = a.w;
-    if (n <= t) return;
+    const int n = info.x, t = info.y, listed = info.z, w = a.w, round = chunk * kWarps;
+    if (info.w == 0) return;
     const int32_t* from = a.from + (size_t)head * a.B;
     const int32_t* to = a.to + (size_t)head * a.B;
     auto pair = [&](int i) { return make_int2(from[i], to[i]); };
@@ -335,19 +360,253 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move(const EvictArgs a, in
     for (int i = 0; i < min(listed, w); i += kMoveThreads)
         early += __syncthreads_count(i + (int)threadIdx.x < min(listed, w) && from[i + threadIdx.x] < t);
     if (part == 0) {
-        move_rows<D, false>(a, head, 0, early, kRound, pair);
+        move_rows<D, kMoveLoads, false>(a, head, 0, early, round, chunk, warp, pair);
         __syncthreads();
-        move_rows<D, true>(a, head, 0, w, kRound, [&](int i) { return make_int2(n - w + i, t - w + i); });
+        move_rows<D, kMoveLoads, true>(a, head, 0, w, kWarps * kBatch, kBatch, warp,
+                                       [&](int i) { return make_int2(n - w + i, t - w + i); });
     }
-    move_rows<D, false>(a, head, early + part * kRound, listed, parts * kRound, pair);
+    move_rows<D, kMoveLoads, false>(a, head, early + part * round, listed, parts * round, chunk, warp, pair);
+}
+
+constexpr int kBins = 256;
+
+template <int C>
+struct PickShared {
+    __align__(16) uint32_t hist[4][kBins];           // of this CTA's keys, a digit a round
+    __align__(16) uint32_t all[2][C > 1 ? C : 1][kBins];   // every CTA's, of the cluster
+    unsigned long long scan[C][kMaxWarps];           // every warp's packed totals for the lists
+    int from[kFew], to[kFew];
+};
+
+// Counts of a run of rows, 16 bits each: kept by their key (gt) or equal to T (eq), below split (low)
+// and not.
+__device__ __forceinline__ unsigned long long pack4(int gt_low, int eq_low, int gt_high, int eq_high) {
+    return (unsigned long long)gt_low | (unsigned long long)eq_low << 16 | (unsigned long long)gt_high << 32 |
+           (unsigned long long)eq_high << 48;
+}
+
+template <int C, int kPer, int D>
+__global__ void __launch_bounds__(kMaxThreads, 1) evict_select(const EvictArgs a) {
+    __shared__ PickShared<C> sh;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
+    const int head = blockIdx.x / C, rank = blockIdx.x % C;
+    const int n = a.c.len(head);
+    const int t = a.budgets ? min(max(a.budgets[head], max(a.s + a.w, 1)), a.B) : a.B;
+    const int w = a.w, s = a.s;
+    const bool full = n > t;
+    const int split = full ? t - w : n;              // rows below keep their places, or are replaced
+    int32_t* src = a.src ? a.src + (size_t)head * a.B : nullptr;
+
+    // rows [j0, j0 + kPer) are this thread's. A key is the weight's bits plus one; 0: no candidate.
+    const int j0 = (rank * threads + tid) * kPer;
+    uint32_t key[kPer];
+    const bool copy = a.acc_out != a.acc;
+    if (copy || full) {
+        const int32_t* table = a.c.table + (size_t)head * a.c.max_pages;
+        float4 x[kPer / 4];
+        size_t row[kPer / 4];
+        bool there[kPer / 4];
+#pragma unroll
+        for (int q = 0; q < kPer / 4; ++q) {
+            const int j = j0 + 4 * q;                // four rows lie in one page
+            const int page = j < n ? table[j >> a.c.page_shift] : -1;
+            there[q] = page >= 0 && page < a.c.num_pages;
+            row[q] = ((size_t)max(page, 0) << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
+        }
+#pragma unroll
+        for (int q = 0; q < kPer / 4; ++q) x[q] = there[q] ? *(const float4*)(a.acc + row[q]) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < kPer / 4; ++q) {
+            const float v[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+            const int j = j0 + 4 * q;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) key[4 * q + i] = key_of(v[i]) + 1;
+            if (there[q] && copy) {
+                if (j + 4 <= split) {
+                    *(float4*)(a.acc_out + row[q]) = x[q];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        if (j + i < split) a.acc_out[row[q] + i] = v[i];
+                }
+            }
+        }
+    }
+    if (src) {
+        // rows that stay (others overwrite theirs when they move), and what lies past the new length
+        const int last = full ? t : n;
+        for (int i = rank * threads + tid; i < a.B; i += C * threads) {
+            if (i < split) src[i] = i;
+            else if (i >= last) src[i] = -1;
+        }
+    }
+    if (!full) {
+        if (rank == 0 && tid == 0) {
+            a.info[head] = make_int4(n, t, 0, 0);
+            a.lens_out[head] = n;                    // (a CTA that reads lens after this clamps to the same n)
+        }
+        return;                                      // the same in every CTA of the cluster
+    }
+    // a bit a row: candidates, and rows below split
+    constexpr uint32_t kAllRows = (1u << kPer) - 1;
+    auto first_bits = [&](int last) { return last <= j0 ? 0u : last - j0 >= kPer ? kAllRows : (1u << (last - j0)) - 1; };
+    const uint32_t cand = first_bits(n - w) & ~first_bits(s), low = first_bits(split);
+    if (cand != kAllRows) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (!(cand >> i & 1)) key[i] = 0;
+    }
+    for (int i = tid; i < 4 * kBins; i += threads) (&sh.hist[0][0])[i] = 0;
+    sync_all<C>();                                   // every CTA of the cluster runs and has read lens
+
+    // ---- T: the largest value that at least kk keys reach
+    const int kk = t - s - w;                        // candidates that stay; there are more than kk
+    uint32_t T = kk > 0 ? 0u : 0xFFFFFFFFu;
+    int above = 0;                                   // keys known to lie above those that T's bits leave open
+    bool exact = kk == 0;                            // just kk keys reach T
+#pragma unroll
+    for (int round = 0; round < 4; ++round) {
+        if (exact) break;
+        const int bits = round < 3 ? 8 : 7, shift = round < 3 ? 23 - 8 * round : 0;
+        uint32_t* hist = sh.hist[round];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            // the bits above this digit are T's, and it is a candidate
+            if (key[i] != 0 && (round == 0 || (key[i] ^ T) >> (shift + bits) == 0))
+                atomicAdd(&hist[key[i] >> shift & ((1u << bits) - 1)], 1u);
+        }
+        __syncthreads();
+        if (C > 1) {                                 // every CTA gets every CTA's counts
+            for (int i = tid; i < C * kBins / 4; i += threads) {
+                uint4* to = (uint4*)sh.all[round & 1][rank] + i % (kBins / 4);
+                *cg::this_cluster().map_shared_rank(to, i / (kBins / 4)) = ((const uint4*)hist)[i % (kBins / 4)];
+            }
+            sync_all<C>();
+        }
+        // lane x: digits 255 - 8 x down to 248 - 8 x; every warp finds the same
+        int bin[8] = {};
+#pragma unroll
+        for (int x = 0; x < C; ++x) {
+            const uint4* from = (const uint4*)((C > 1 ? sh.all[round & 1][x] : hist) + kBins - 8 - 8 * lane);
+            const uint4 lo = from[0], hi = from[1];
+            bin[0] += hi.w, bin[1] += hi.z, bin[2] += hi.y, bin[3] += hi.x;
+            bin[4] += lo.w, bin[5] += lo.z, bin[6] += lo.y, bin[7] += lo.x;
+        }
+        int inc = ((bin[0] + bin[1]) + (bin[2] + bin[3])) + ((bin[4] + bin[5]) + (bin[6] + bin[7]));
+        const int sum = inc;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const int want = kk - above;                 // the want-th key from the top is T
+        const int owner = __ffs(__ballot_sync(0xffffffffu, inc >= want)) - 1;   // there is one: more than kk keys
+        int before = inc - sum, digit = 255 - 8 * lane, count = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            count = bin[i];
+            if (before + count >= want) break;
+            before += count;
+            --digit;
+        }
+        T |= (uint32_t)__shfl_sync(0xffffffffu, digit, owner) << shift;
+        above += __shfl_sync(0xffffffffu, before, owner);
+        exact = above + __shfl_sync(0xffffffffu, count, owner) == kk;
+    }
+    // rows whose key is T that stay, lowest first; none is needed where just kk keys reach T
+    const int need_eq = exact ? 0 : kk - above;
+    uint32_t gt = 0, eqm = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        gt |= (exact ? key[i] >= T : key[i] > T) ? 1u << i : 0u;
+        eqm |= key[i] == T ? 1u << i : 0u;
+    }
+    if (exact) eqm = 0;
+
+    // ---- places in the lists
+    const unsigned long long mine = pack4(__popc(gt & low), __popc(eqm & low), __popc(gt & ~low), __popc(eqm & ~low));
+    unsigned long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    const unsigned long long whole = __shfl_sync(0xffffffffu, inc, 31);
+    if (C > 1) {
+        if (lane < C) *cg::this_cluster().map_shared_rank(&sh.scan[rank][warp], lane) = whole;
+    } else if (lane == 0) {
+        sh.scan[0][warp] = whole;
+    }
+    sync_all<C>();
+    int b_gt_low = 0, b_eq_low = 0, b_gt_high = 0, b_eq_high = 0, all_gt_high = 0, all_eq_low = 0, all_eq_high = 0;
+#pragma unroll
+    for (int x = 0; x < C; ++x) {
+        const unsigned long long v = lane < warps ? sh.scan[x][lane] : 0ull;
+        const bool before = x < rank || (x == rank && lane < warp);
+        const int gl = (int)(v & 0xFFFF), el = (int)(v >> 16 & 0xFFFF), gh = (int)(v >> 32 & 0xFFFF), eh = (int)(v >> 48);
+        b_gt_low += before ? gl : 0;
+        b_eq_low += before ? el : 0;
+        b_gt_high += before ? gh : 0;
+        b_eq_high += before ? eh : 0;
+        all_eq_low += el;
+        all_gt_high += gh;
+        all_eq_high += eh;
+    }
+    const unsigned long long excl = inc - mine;      // of the lanes before this one
+    b_gt_low = __reduce_add_sync(0xffffffffu, b_gt_low) + (int)(excl & 0xFFFF);
+    b_eq_low = __reduce_add_sync(0xffffffffu, b_eq_low) + (int)(excl >> 16 & 0xFFFF);
+    b_gt_high = __reduce_add_sync(0xffffffffu, b_gt_high) + (int)(excl >> 32 & 0xFFFF);
+    b_eq_high = __reduce_add_sync(0xffffffffu, b_eq_high) + (int)(excl >> 48);
+    all_eq_low = __reduce_add_sync(0xffffffffu, all_eq_low);
+    all_gt_high = __reduce_add_sync(0xffffffffu, all_gt_high);
+    all_eq_high = __reduce_add_sync(0xffffffffu, all_eq_high);
+    // equal rows stay from the lowest on, and the low ones come first
+    const int listed = all_gt_high + min(all_eq_low + all_eq_high, need_eq) - min(all_eq_low, need_eq);
+    const int eq = b_eq_low + b_eq_high, room = max(0, need_eq - eq);    // equal rows before; of this thread's, that stay
+    const int kept_low = b_gt_low + min(b_eq_low, need_eq);
+    const int kept_high = b_gt_high + min(eq, need_eq) - min(b_eq_low, need_eq);
+    while (__popc(eqm) > room) eqm &= ~(1u << (31 - __clz(eqm)));         // drops the highest
+    const uint32_t kept = gt | eqm;
+    int32_t* from = a.from + (size_t)head * a.B;
+    int32_t* to = a.to + (size_t)head * a.B;
+    const bool here = C == 1 && listed + w <= kFew;  // copied below
+    // evicted places: candidates before this thread's rows less those kept
+    int at = max(0, min(j0, n - w) - s) - kept_low;
+    for (uint32_t m = cand & low & ~kept; m; m &= m - 1, ++at) {
+        const int j = j0 + __ffs(m) - 1;
+        if (here) sh.to[at] = j;
+        else if (KVP_CHECK(at >= 0 && at < a.B, 701, head, at)) to[at] = j;
+    }
+    at = kept_high;
+    for (uint32_t m = kept & ~low; m; m &= m - 1, ++at) {
+        const int j = j0 + __ffs(m) - 1;
+        if (here) sh.from[at] = j;
+        else if (KVP_CHECK(at < a.B, 702, head, at)) from[at] = j;
+    }
+    if (rank == 0 && tid == 0) {
+        a.info[head] = make_int4(n, t, listed, !here);
+        a.lens_out[head] = t;
+    }
+    if (C > 1) {
+        cg::this_cluster().sync();                   // shared memory outlives its readers
+    } else if (here) {
+        __syncthreads();
+        constexpr int kBatch = batch_rows<D>(kFewLoads);
+        move_rows<D, kFewLoads, false>(a, head, 0, listed, warps * kBatch, kBatch, warp,
+                                       [&](int i) { return make_int2(sh.from[i], sh.to[i]); });
+        __syncthreads();
+        move_rows<D, kFewLoads, true>(a, head, 0, w, warps * kBatch, kBatch, warp,
+                                      [&](int i) { return make_int2(n - w + i, t - w + i); });
+    }
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-template <int C>
-cudaError_t launch_select_c(const EvictArgs& a, int threads, size_t smem, cudaStream_t st) {
-    const cudaError_t e = allow_dynamic_smem((const void*)evict_select<C>, smem);
-    if (e != cudaSuccess) return e;
+// `kernel` with clusters of C CTAs, one per head.
+cudaError_t launch_heads(void (*kernel)(const EvictArgs), const EvictArgs& a, int C, int threads, size_t smem,
+                         cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.c.heads * C));
     cfg.blockDim = dim3((unsigned)threads);
@@ -362,7 +621,14 @@ cudaError_t launch_select_c(const EvictArgs& a, int threads, size_t smem, cudaSt
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, evict_select<C>, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int C, int kPer>
+cudaError_t launch_select(const EvictArgs& a, int head_dim, int threads, cudaStream_t st) {
+    // (a cluster copies no rows: it does not depend on their length)
+    return launch_heads(C > 1 || head_dim == 128 ? evict_select<C, kPer, 128> : evict_select<C, kPer, C == 1 ? 64 : 128>, a,
+                        C, threads, 0, st);
 }
 
 }  // namespace
@@ -393,22 +659,35 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
     a.info = (int4*)ws;
     a.from = (int32_t*)(ws + align256((size_t)heads * sizeof(int4)));
     a.to = (int32_t*)(ws + align256((size_t)heads * sizeof(int4)) + align256((size_t)heads * e.budget * 4));
+    a.slice = 0;
     // CTAs per head: 8 where the heads alone would leave most SMs idle and rows are many
     const int sms = num_sms();
-    const int C = (long long)cap > 4096 && (heads * 2 < sms || cap > kSliceCap) ? 8 : 1;
-    const int slice = ((cap + C - 1) / C + 15) / 16 * 16;
-    a.slice = slice <= kSliceCap ? slice : 0;
-    const size_t smem = (size_t)a.slice * 4;
-    int threads = 128;
-    while (threads < kMaxThreads && threads * 8 < slice) threads *= 2;
-    cudaError_t err = C == 8 ? launch_select_c<8>(a, threads, smem, st) : launch_select_c<1>(a, threads, smem, st);
+    const int C = cap > 4096 && (heads * 2 < sms || cap > kMaxThreads * kPerMost) ? 8 : 1;
+    const int slice = (cap + C - 1) / C;
+    cudaError_t err;
+    if (slice <= kMaxThreads * kPerMost) {
+        // a cluster, whose CTAs have an SM each: 8 keys a thread, 16 once that takes more than 1024
+        // threads; else 16, for several CTAs an SM
+        const int per = C == 8 && slice <= kMaxThreads * 8 ? 8 : kPerMost;
+        const int threads = std::max(64, (slice + per * 32 - 1) / (per * 32) * 32);
+        err = C == 8 ? (per == 8 ? launch_select<8, 8>(a, s.head_dim, threads, st) : launch_select<8, 16>(a, s.head_dim, threads, st))
+                     : launch_select<1, 16>(a, s.head_dim, threads, st);
+    } else {
+        a.slice = (slice + 15) / 16 * 16 <= kSliceCap ? (slice + 15) / 16 * 16 : 0;
+        err = allow_dynamic_smem((const void*)evict_select_long<8>, (size_t)a.slice * 4);
+        if (err == cudaSuccess) err = launch_heads(evict_select_long<8>, a, 8, kMaxThreads, (size_t)a.slice * 4, st);
+    }
     if (err != cudaSuccess) return err;
-    // rows that can change places per head, and blocks enough to fill the card with them
-    const int round = kMoveThreads / (s.head_dim / 4) * kMoveRows;
+    // rows that can change places per head; blocks enough to fill the card with them
     const int most = std::min(e.budget, std::max(0, cap - e.budget));
-    const int parts = std::max(1, std::min((most + round - 1) / round, (sms * 6 + heads - 1) / heads));
-    return s.head_dim == 128 ? launch_dependent(evict_move<128>, heads * parts, kMoveThreads, 0, st, a, parts)
-                             : launch_dependent(evict_move<64>, heads * parts, kMoveThreads, 0, st, a, parts);
+    if (C == 1 && !budgets && most + e.window <= kFew) return cudaSuccess;   // evict_select copies them all
+    // rows a warp takes at a time: 32, fewer where that would leave warps without any
+    const int warps = sms * 3 * (kMoveThreads / 32), batch = s.head_dim == 128 ? batch_rows<128>(kMoveLoads) : batch_rows<64>(kMoveLoads);
+    const int chunk = (int)std::min<long long>(32, std::max<long long>(batch, (long long)heads * most / warps / batch * batch));
+    const int round = chunk * (kMoveThreads / 32);
+    const int parts = std::max(1, std::min((most + round - 1) / round, (sms * 8 + heads - 1) / heads));
+    return s.head_dim == 128 ? launch_dependent(evict_move<128>, heads * parts, kMoveThreads, 0, st, a, parts, chunk)
+                             : launch_dependent(evict_move<64>, heads * parts, kMoveThreads, 0, st, a, parts, chunk);
 }
 
 #ifdef KVP_CHECKS
