@@ -35,7 +35,7 @@ constexpr int kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kSliceCap = 48 * 1024;     // keys a CTA of evict_select_long holds in shared memory
 constexpr int kPerMost = 16;             // keys a thread of evict_select holds
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 256, kMoveCtas = 3;   // of evict_move: threads, CTAs an SM
 constexpr int kMoveLoads = 8;            // 16-byte loads a lane has in flight in evict_move,
 constexpr int kFewLoads = 4;             // and in evict_select, whose threads may have 64 registers
 constexpr int kFew = 256;                // rows that evict_select copies itself (one CTA a head)
@@ -51,7 +51,7 @@ struct EvictArgs {
     int32_t* src;             // NULL: not wanted
     int B, s, w;
     // workspace
-    int4* info;               // [heads]: n, t, rows listed, whether they are still to be copied
+    int4* info;               // [heads]: n, t, rows listed, 1 + those below t (0: nothing left to copy)
     int32_t* from;            // [heads][B]: listed rows, ascending
     int32_t* to;              // [heads][B]: the places they move to, ascending
     int slice;                // evict_select_long: keys that shared memory holds per CTA; 0: read again each round
@@ -78,6 +78,10 @@ __device__ __forceinline__ void sync_all() {
     if (C > 1) cg::this_cluster().sync();
     else __syncthreads();
 }
+
+// The cluster's barrier in two halves: all threads of the cluster arrive, all wait.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <int C>
 __global__ void __launch_bounds__(kMaxThreads, 1) evict_select_long(const EvictArgs a) {
@@ -254,10 +258,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) evict_select_long(const EvictA
             eq = e0;
             kept_low = l0;
             kept_high = h0;
-            if (lane == 0) {
-                a.info[head] = make_int4(n, t, listed, 1);
-                a.lens_out[head] = t;                 // every CTA has read lens
-            }
+            if (lane == 0) a.lens_out[head] = t;      // every CTA has read lens
         }
     }
     int32_t* from = a.from + (size_t)head * a.B;
@@ -289,7 +290,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) evict_select_long(const EvictA
     }
     if (src)
         for (int i = rank * threads + tid; i < s; i += C * threads) src[i] = i;
-    if (C > 1) cg::this_cluster().sync();             // shared memory outlives its readers
+    // listed rows below t, for evict_move: the first of the list
+    cg::this_cluster().sync();                        // the lists are there
+    if (rank == 0 && warp == 0) {
+        int early = 0;
+        for (int i = lane; i - lane < min(listed, w); i += 32)
+            early += __popc(__ballot_sync(0xffffffffu, i < min(listed, w) && from[i] < t));
+        if (lane == 0) a.info[head] = make_int4(n, t, listed, 1 + early);
+    }
 }
 
 // Copies rows pair(i) = (source, place) of a head, i in [first, last), `chunk` (up to 32) at a time by
@@ -342,30 +350,27 @@ __host__ __device__ constexpr int batch_rows(int loads) {
     return loads * (32 / (D / 4));
 }
 
-// parts blocks per head: the listed rows that lie past t are dealt over all of them; block 0 first
-// copies those below t, then the window.
+// parts + 1 blocks per head: the first copies the listed rows below t, then the window; the others
+// share the rest of the list.
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) evict_move(const EvictArgs a, int parts, int chunk) {
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move(const EvictArgs a, int parts, int chunk) {
     constexpr int kWarps = kMoveThreads / 32, kBatch = batch_rows<D>(kMoveLoads);
     ptx::grid_dependency_wait();
-    const int head = blockIdx.x / parts, part = blockIdx.x % parts, warp = threadIdx.x >> 5;
+    const int head = blockIdx.x / (parts + 1), part = blockIdx.x % (parts + 1), warp = threadIdx.x >> 5;
     const int4 info = a.info[head];
-    const int n = info.x, t = info.y, listed = info.z, w = a.w, round = chunk * kWarps;
-    if (info.w == 0) return;
+    const int n = info.x, t = info.y, listed = info.z, early = info.w - 1, w = a.w, round = chunk * kWarps;
+    if (early < 0) return;
     const int32_t* from = a.from + (size_t)head * a.B;
     const int32_t* to = a.to + (size_t)head * a.B;
     auto pair = [&](int i) { return make_int2(from[i], to[i]); };
-    // listed rows in [t - w, t): the first of the list
-    int early = 0;
-    for (int i = 0; i < min(listed, w); i += kMoveThreads)
-        early += __syncthreads_count(i + (int)threadIdx.x < min(listed, w) && from[i + threadIdx.x] < t);
     if (part == 0) {
-        move_rows<D, kMoveLoads, false>(a, head, 0, early, round, chunk, warp, pair);
+        move_rows<D, kMoveLoads, false>(a, head, 0, early, kWarps * kBatch, kBatch, warp, pair);
         __syncthreads();
         move_rows<D, kMoveLoads, true>(a, head, 0, w, kWarps * kBatch, kBatch, warp,
                                        [&](int i) { return make_int2(n - w + i, t - w + i); });
+    } else {
+        move_rows<D, kMoveLoads, false>(a, head, early + (part - 1) * round, listed, parts * round, chunk, warp, pair);
     }
-    move_rows<D, kMoveLoads, false>(a, head, early + part * round, listed, parts * round, chunk, warp, pair);
 }
 
 constexpr int kBins = 256;
@@ -396,6 +401,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) evict_select(const EvictArgs a
     const int t = a.budgets ? min(max(a.budgets[head], max(a.s + a.w, 1)), a.B) : a.B;
     const int w = a.w, s = a.s;
     const bool full = n > t;
+    if (C > 1) cluster_arrive();                     // this thread has read lens
     const int split = full ? t - w : n;              // rows below keep their places, or are replaced
     int32_t* src = a.src ? a.src + (size_t)head * a.B : nullptr;
 
@@ -443,9 +449,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) evict_select(const EvictArgs a
         }
     }
     if (!full) {
+        if (C > 1) cluster_wait();
         if (rank == 0 && tid == 0) {
             a.info[head] = make_int4(n, t, 0, 0);
-            a.lens_out[head] = n;                    // (a CTA that reads lens after this clamps to the same n)
+            a.lens_out[head] = n;
         }
         return;                                      // the same in every CTA of the cluster
     }
@@ -459,7 +466,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) evict_select(const EvictArgs a
             if (!(cand >> i & 1)) key[i] = 0;
     }
     for (int i = tid; i < 4 * kBins; i += threads) (&sh.hist[0][0])[i] = 0;
-    sync_all<C>();                                   // every CTA of the cluster runs and has read lens
+    if (C > 1) cluster_wait();                       // every CTA of the cluster runs and has read lens
+    __syncthreads();
 
     // ---- T: the largest value that at least kk keys reach
     const int kk = t - s - w;                        // candidates that stay; there are more than kk
@@ -585,13 +593,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) evict_select(const EvictArgs a
         if (here) sh.from[at] = j;
         else if (KVP_CHECK(at < a.B, 702, head, at)) from[at] = j;
     }
-    if (rank == 0 && tid == 0) {
-        a.info[head] = make_int4(n, t, listed, !here);
-        a.lens_out[head] = t;
-    }
-    if (C > 1) {
-        cg::this_cluster().sync();                   // shared memory outlives its readers
-    } else if (here) {
+    if (j0 <= t && t < j0 + kPer)                    // row t is this thread's
+        a.info[head] = make_int4(n, t, listed, here ? 0 : 1 + kept_high + __popc(kept & ~low & first_bits(t)));
+    if (rank == 0 && tid == 0) a.lens_out[head] = t;
+    // (the cluster's CTAs write into one another's shared memory only before the last sync_all)
+    if (here) {
         __syncthreads();
         constexpr int kBatch = batch_rows<D>(kFewLoads);
         move_rows<D, kFewLoads, false>(a, head, 0, listed, warps * kBatch, kBatch, warp,
@@ -682,12 +688,12 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
     const int most = std::min(e.budget, std::max(0, cap - e.budget));
     if (C == 1 && !budgets && most + e.window <= kFew) return cudaSuccess;   // evict_select copies them all
     // rows a warp takes at a time: 32, fewer where that would leave warps without any
-    const int warps = sms * 3 * (kMoveThreads / 32), batch = s.head_dim == 128 ? batch_rows<128>(kMoveLoads) : batch_rows<64>(kMoveLoads);
+    const int warps = sms * kMoveCtas * (kMoveThreads / 32), batch = s.head_dim == 128 ? batch_rows<128>(kMoveLoads) : batch_rows<64>(kMoveLoads);
     const int chunk = (int)std::min<long long>(32, std::max<long long>(batch, (long long)heads * most / warps / batch * batch));
     const int round = chunk * (kMoveThreads / 32);
-    const int parts = std::max(1, std::min((most + round - 1) / round, (sms * 8 + heads - 1) / heads));
-    return s.head_dim == 128 ? launch_dependent(evict_move<128>, heads * parts, kMoveThreads, 0, st, a, parts, chunk)
-                             : launch_dependent(evict_move<64>, heads * parts, kMoveThreads, 0, st, a, parts, chunk);
+    const int parts = std::max(1, std::min((most + round - 1) / round, sms * kMoveCtas / heads - 1));
+    return s.head_dim == 128 ? launch_dependent(evict_move<128>, heads * (parts + 1), kMoveThreads, 0, st, a, parts, chunk)
+                             : launch_dependent(evict_move<64>, heads * (parts + 1), kMoveThreads, 0, st, a, parts, chunk);
 }
 
 #ifdef KVP_CHECKS
