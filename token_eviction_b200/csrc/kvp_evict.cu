@@ -34,11 +34,11 @@ namespace {
 constexpr int kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kSliceCap = 48 * 1024;     // keys a CTA of evict_select_long holds in shared memory
+constexpr int kManyThreads = 384;         // most threads of the CTAs that share an SM with others
 constexpr int kPerMost = 16;             // keys a thread of evict_select holds
 constexpr int kMoveThreads = 256, kMoveCtas = 3;   // of evict_move: threads, CTAs an SM
-constexpr int kMoveLoads = 8;            // 16-byte loads a lane has in flight in evict_move,
-constexpr int kFewLoads = 4;             // and in evict_select, whose threads may have 64 registers
-constexpr int kFew = 256;                // rows that evict_select copies itself (one CTA a head)
+constexpr int kMoveLoads = 8;            // 16-byte loads a lane of evict_move has in flight
+constexpr int kFew = 64;                 // rows past t - w up to which evict_select copies them itself (one CTA a head)
 
 struct EvictArgs {
     CacheView c;
@@ -54,6 +54,7 @@ struct EvictArgs {
     int4* info;               // [heads]: n, t, rows listed, 1 + those below t (0: nothing left to copy)
     int32_t* from;            // [heads][B]: listed rows, ascending
     int32_t* to;              // [heads][B]: the places they move to, ascending
+    int row_chunks;           // d / 8
     int slice;                // evict_select_long: keys that shared memory holds per CTA; 0: read again each round
 };
 
@@ -380,7 +381,9 @@ struct PickShared {
     __align__(16) uint32_t hist[4][kBins];           // of this CTA's keys, a digit a round
     __align__(16) uint32_t all[2][C > 1 ? C : 1][kBins];   // every CTA's, of the cluster
     unsigned long long scan[C][kMaxWarps];           // every warp's packed totals for the lists
-    int from[kFew], to[kFew];
+    int from[kFew], to[kFew];                        // listed rows, where they are copied here
+    long long row[kFew];                             // rows [t - w, n): where they lie (-1: no page),
+    float weight[kFew];                              // and their weights
 };
 
 // Counts of a run of rows, 16 bits each: kept by their key (gt) or equal to T (eq), below split (low)
@@ -390,8 +393,9 @@ __device__ __forceinline__ unsigned long long pack4(int gt_low, int eq_low, int 
            (unsigned long long)eq_high << 48;
 }
 
-template <int C, int kPer, int D>
-__global__ void __launch_bounds__(kMaxThreads, 1) evict_select(const EvictArgs a) {
+template <int C, int kPer, int kThreads = kMaxThreads, int kCtas = 1>
+__global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs a) {
+    extern __shared__ __align__(16) uint32_t keys[];   // (C = 1) rows [t - w, n), where they are few
     __shared__ PickShared<C> sh;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
@@ -404,6 +408,26 @@ __global__ void __launch_bounds__(kMaxThreads, 1) evict_select(const EvictArgs a
     if (C > 1) cluster_arrive();                     // this thread has read lens
     const int split = full ? t - w : n;              // rows below keep their places, or are replaced
     int32_t* src = a.src ? a.src + (size_t)head * a.B : nullptr;
+
+    // With few rows past t - w, all that can move are fetched while the rest is worked out.
+    const bool here = C == 1 && full && n - split <= kFew;
+    const int d_chunks = a.row_chunks;               // 16-byte chunks of a row of keys (then as many of values)
+    if (here) {
+        for (int r = tid; r < n - split; r += threads) {
+            const long long row = a.c.row(head, split + r);
+            sh.row[r] = row;
+            sh.weight[r] = row >= 0 ? a.acc[row] : 0.f;
+        }
+        for (int r = warp; r < n - split; r += warps) {   // a warp a row
+            const long long row = a.c.row(head, split + r);
+            if (row < 0 || lane >= 2 * d_chunks) continue;
+            const uint4* from = (lane < d_chunks ? a.k_pages : a.v_pages) + row * d_chunks + (lane & (d_chunks - 1));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             ptx::smem_u32((uint4*)keys + r * 2 * d_chunks + lane)),
+                         "l"(from)
+                         : "memory");
+        }
+    }
 
     // rows [j0, j0 + kPer) are this thread's. A key is the weight's bits plus one; 0: no candidate.
     const int j0 = (rank * threads + tid) * kPer;
@@ -579,7 +603,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) evict_select(const EvictArgs a
     const uint32_t kept = gt | eqm;
     int32_t* from = a.from + (size_t)head * a.B;
     int32_t* to = a.to + (size_t)head * a.B;
-    const bool here = C == 1 && listed + w <= kFew;  // copied below
     // evicted places: candidates before this thread's rows less those kept
     int at = max(0, min(j0, n - w) - s) - kept_low;
     for (uint32_t m = cand & low & ~kept; m; m &= m - 1, ++at) {
@@ -598,13 +621,21 @@ __global__ void __launch_bounds__(kMaxThreads, 1) evict_select(const EvictArgs a
     if (rank == 0 && tid == 0) a.lens_out[head] = t;
     // (the cluster's CTAs write into one another's shared memory only before the last sync_all)
     if (here) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
-        constexpr int kBatch = batch_rows<D>(kFewLoads);
-        move_rows<D, kFewLoads, false>(a, head, 0, listed, warps * kBatch, kBatch, warp,
-                                       [&](int i) { return make_int2(sh.from[i], sh.to[i]); });
-        __syncthreads();
-        move_rows<D, kFewLoads, true>(a, head, 0, w, warps * kBatch, kBatch, warp,
-                                      [&](int i) { return make_int2(n - w + i, t - w + i); });
+        // a warp a row: the listed ones, then the window; all that is read is in shared memory
+        for (int i = warp; i < listed + w; i += warps) {
+            const bool is_listed = i < listed;
+            const int r = is_listed ? sh.from[i] - split : n - w - split + i - listed;     // source
+            const int place = is_listed ? sh.to[i] : split + i - listed;
+            const long long to = is_listed ? a.c.row(head, place) : sh.row[i - listed];
+            if (src && lane == 0) src[place] = split + r;
+            if (sh.row[r] < 0 || to < 0) continue;
+            if (!KVP_CHECK(to < ((long long)a.c.num_pages << a.c.page_shift), 704, head, place)) continue;
+            if (lane < 2 * d_chunks)
+                ((lane < d_chunks ? a.k_pages : a.v_pages) + to * d_chunks)[lane & (d_chunks - 1)] = ((const uint4*)keys)[r * 2 * d_chunks + lane];
+            if (lane == 0) a.acc_out[to] = sh.weight[r];
+        }
     }
 }
 
@@ -628,13 +659,6 @@ cudaError_t launch_heads(void (*kernel)(const EvictArgs), const EvictArgs& a, in
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
-}
-
-template <int C, int kPer>
-cudaError_t launch_select(const EvictArgs& a, int head_dim, int threads, cudaStream_t st) {
-    // (a cluster copies no rows: it does not depend on their length)
-    return launch_heads(C > 1 || head_dim == 128 ? evict_select<C, kPer, 128> : evict_select<C, kPer, C == 1 ? 64 : 128>, a,
-                        C, threads, 0, st);
 }
 
 }  // namespace
@@ -666,6 +690,7 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
     a.from = (int32_t*)(ws + align256((size_t)heads * sizeof(int4)));
     a.to = (int32_t*)(ws + align256((size_t)heads * sizeof(int4)) + align256((size_t)heads * e.budget * 4));
     a.slice = 0;
+    a.row_chunks = s.head_dim / 8;
     // CTAs per head: 8 where the heads alone would leave most SMs idle and rows are many
     const int sms = num_sms();
     const int C = cap > 4096 && (heads * 2 < sms || cap > kMaxThreads * kPerMost) ? 8 : 1;
@@ -674,10 +699,13 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
     if (slice <= kMaxThreads * kPerMost) {
         // a cluster, whose CTAs have an SM each: 8 keys a thread, 16 once that takes more than 1024
         // threads; else 16, for several CTAs an SM
-        const int per = C == 8 && slice <= kMaxThreads * 8 ? 8 : kPerMost;
+        const int per = slice <= (C == 8 ? kMaxThreads : kManyThreads) * 8 ? 8 : kPerMost;
         const int threads = std::max(64, (slice + per * 32 - 1) / (per * 32) * 32);
-        err = C == 8 ? (per == 8 ? launch_select<8, 8>(a, s.head_dim, threads, st) : launch_select<8, 16>(a, s.head_dim, threads, st))
-                     : launch_select<1, 16>(a, s.head_dim, threads, st);
+        if (C == 8) {
+            err = launch_heads(per == 8 ? evict_select<8, 8> : evict_select<8, kPerMost>, a, C, threads, 0, st);
+        } else {
+            err = launch_heads(per == 8 ? evict_select<1, 8, kManyThreads, 3> : evict_select<1, kPerMost>, a, C, threads, (size_t)kFew * s.head_dim * 4, st);
+        }
     } else {
         a.slice = (slice + 15) / 16 * 16 <= kSliceCap ? (slice + 15) / 16 * 16 : 0;
         err = allow_dynamic_smem((const void*)evict_select_long<8>, (size_t)a.slice * 4);
@@ -685,8 +713,8 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
     }
     if (err != cudaSuccess) return err;
     // rows that can change places per head; blocks enough to fill the card with them
+    if (C == 1 && !budgets && cap - e.budget + e.window <= kFew) return cudaSuccess;   // evict_select copies them all
     const int most = std::min(e.budget, std::max(0, cap - e.budget));
-    if (C == 1 && !budgets && most + e.window <= kFew) return cudaSuccess;   // evict_select copies them all
     // rows a warp takes at a time: 32, fewer where that would leave warps without any
     const int warps = sms * kMoveCtas * (kMoveThreads / 32), batch = s.head_dim == 128 ? batch_rows<128>(kMoveLoads) : batch_rows<64>(kMoveLoads);
     const int chunk = (int)std::min<long long>(32, std::max<long long>(batch, (long long)heads * most / warps / batch * batch));
