@@ -1,9 +1,9 @@
 // Appending rows to a paged cache: row i of a head's new rows becomes its row len + i.
 //
-// A bit copy, bound by HBM when rows are many and by the launch when there is one per head.
-// A warp takes kRows rows at a time; the 2 d * 2 bytes of a row's key and value are 32 (d = 128)
-// or 16 (d = 64) pieces of 16 bytes, one a lane, so every load and store covers whole rows, and
-// the loads of all kRows rows are issued before the first store.
+// A bit copy, bound by HBM when rows are many and by the launch and three dependent reads (length,
+// page, then the store) when there is one per head. A row's key and value are 32 (d = 128) or 16
+// (d = 64) pieces of 16 bytes; a warp takes kLoads loads of them, all issued before anything is
+// looked up, while a lane a row finds where the row goes and writes its weight.
 #include <algorithm>
 
 #include "kvp_cache.cuh"
@@ -12,8 +12,8 @@
 namespace kvp {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRows = 4;      // rows in flight per group of lanes
+constexpr int kThreads = 128;
+constexpr int kLoads = 8;     // 16-byte loads a lane has in flight
 
 struct AppendArgs {
     CacheView c;
@@ -29,26 +29,43 @@ struct AppendArgs {
     long long rows;          // b * hkv * n
 };
 
-// Row r of the flattened new rows: its head and its place among that head's new rows (head = -1:
-// past the sequence's counts).
+// Row r of the flattened new rows (a lane a row; all lanes of the warp take part, r < 0: none): its head
+// (-1: past the sequence's counts, or none) and its place among that head's new rows.
 __device__ __forceinline__ void place_of(const AppendArgs& a, long long r, int& head, int& i) {
     if (a.counts == nullptr) {
-        head = (int)(r / a.n);
+        head = r < 0 ? -1 : (int)(r / a.n);
         i = (int)(r - (long long)head * a.n);
         return;
     }
     const long long per = (long long)a.hkv * a.n;
-    const int seq = (int)(r / per);
-    long long left = r - seq * per;
+    const int lane = threadIdx.x & 31, seq = r < 0 ? -1 : (int)(r / per);
+    const long long left = r - seq * per;
     head = -1;
-    for (int h = 0; h < a.hkv; ++h) {
-        const int cnt = max(0, a.counts[(size_t)seq * a.hkv + h]);
-        if (left < cnt) {
-            head = seq * a.hkv + h;
-            i = (int)left;
-            return;
+    i = 0;
+    // the warp's rows lie in a few sequences: for each, prefix sums of its heads' counts, 32 at a time
+    for (unsigned todo = __ballot_sync(0xffffffffu, seq >= 0); todo;) {
+        const int s = __shfl_sync(0xffffffffu, seq, __ffs(todo) - 1);
+        long long base = 0;                           // rows of the heads before
+        for (int h0 = 0; h0 < a.hkv; h0 += 32) {
+            long long end = h0 + lane < a.hkv ? max(0, a.counts[(size_t)s * a.hkv + h0 + lane]) : 0;
+            const long long cnt = end;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o) end += y;
+            }
+            end += base;
+            const int heads = min(32, a.hkv - h0);
+            for (int x = 0; x < heads; ++x) {
+                const long long e = __shfl_sync(0xffffffffu, end, x), b = e - __shfl_sync(0xffffffffu, cnt, x);
+                if (seq == s && left >= b && left < e) {
+                    head = s * a.hkv + h0 + x;
+                    i = (int)(left - b);
+                }
+            }
+            base = __shfl_sync(0xffffffffu, end, 31);
         }
-        left -= cnt;
+        todo &= ~__ballot_sync(0xffffffffu, seq == s);
     }
 }
 
@@ -65,38 +82,42 @@ __device__ __forceinline__ int rows_of(const int32_t* counts, int hkv, int n, in
     return cnt;
 }
 
+// Rows that a warp's kLoads loads cover.
+template <int D>
+__host__ __device__ constexpr int batch_rows() {
+    return kLoads * (32 / (D / 4));
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) append_rows(const AppendArgs a) {
-    constexpr int kPieces = D / 8;                 // 16-byte pieces of a key
-    constexpr int kLanes = 2 * kPieces;            // lanes that carry one row
+    constexpr int kPieces = D / 8, kLanes = 2 * kPieces, kAtOnce = 32 / kLanes, kBatch = batch_rows<D>();
     ptx::grid_dependency_wait();
-    const int lane = threadIdx.x % kLanes, piece = lane % kPieces;
-    const bool is_v = lane >= kPieces;
-    const uint4* from = is_v ? a.v_new : a.k_new;
-    uint4* to = is_v ? a.v_pages : a.k_pages;
-    const long long groups = (long long)gridDim.x * (kThreads / kLanes);
-    const long long g0 = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-    for (long long base = g0 * kRows; base < a.rows; base += groups * kRows) {
-        uint4 piece_of[kRows];
-        long long dst[kRows];
+    ptx::launch_dependents();
+    const int lane = threadIdx.x & 31, piece = lane % kPieces, sub = lane / kLanes;
+    const bool is_v = (lane / kPieces) & 1;
+    const uint4* from = (is_v ? a.v_new : a.k_new) + piece;
+    uint4* to = (is_v ? a.v_pages : a.k_pages) + piece;
+    const long long warps = (long long)gridDim.x * (kThreads / 32);
+    const long long w0 = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    for (long long base = w0 * kBatch; base < a.rows; base += warps * kBatch) {
+        const int here = (int)min((long long)kBatch, a.rows - base);
+        uint4 x[kLoads];
 #pragma unroll
-        for (int t = 0; t < kRows; ++t) {
-            dst[t] = -1;
-            const long long r = base + t;
-            if (r >= a.rows) continue;
-            piece_of[t] = from[r * kPieces + piece];
-            int head, i = 0;
-            place_of(a, r, head, i);
-            if (head < 0) continue;
+        for (int l = 0; l < kLoads; ++l)
+            if (l * kAtOnce + sub < here) x[l] = from[(base + l * kAtOnce + sub) * kPieces];
+        int head, i;
+        place_of(a, lane < here ? base + lane : -1, head, i);
+        long long dst = -1;
+        if (head >= 0) {
             const long long j = (long long)a.c.len(head) + i;
-            if (j < a.c.cap()) dst[t] = a.c.row(head, (int)j);
+            if (j < a.c.cap()) dst = a.c.row(head, (int)j);
+            if (!KVP_CHECK(dst < ((long long)a.c.num_pages << a.c.page_shift), 501, (int)base, lane)) dst = -1;
+            if (dst >= 0 && a.acc) a.acc[dst] = a.weight ? a.weight[base + lane] : 0.f;
         }
 #pragma unroll
-        for (int t = 0; t < kRows; ++t) {
-            if (dst[t] < 0) continue;
-            if (!KVP_CHECK(dst[t] < ((long long)a.c.num_pages << a.c.page_shift), 501, (int)base, t)) continue;
-            to[dst[t] * kPieces + piece] = piece_of[t];
-            if (lane == 0 && a.acc) a.acc[dst[t]] = a.weight ? a.weight[base + t] : 0.f;
+        for (int l = 0; l < kLoads; ++l) {
+            const long long d = __shfl_sync(0xffffffffu, dst, (l * kAtOnce + sub) & 31);
+            if (l * kAtOnce + sub < here && d >= 0) to[d * kPieces] = x[l];
         }
     }
     if (a.lens_out) {
@@ -135,7 +156,7 @@ cudaError_t launch_append(const kvp_cache_shape& s, const uint16_t* k_new, const
     a.hkv = s.hkv;
     a.n = n;
     a.rows = (long long)a.c.heads * n;
-    const int per_cta = kThreads / (s.head_dim / 4) * kRows;
+    const int per_cta = (s.head_dim == 128 ? batch_rows<128>() : batch_rows<64>()) * (kThreads / 32);
     const long long want = std::max<long long>(1, (a.rows + per_cta - 1) / per_cta);
     const int grid = (int)std::min<long long>(want, (long long)num_sms() * 8);
     cudaError_t e = s.head_dim == 128 ? launch_dependent(append_rows<128>, grid, kThreads, 0, st, a)
