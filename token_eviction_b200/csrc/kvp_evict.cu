@@ -54,6 +54,8 @@ struct EvictArgs {
     int4* info;               // [heads]: n, t, rows listed, 1 + those below t (0: nothing left to copy)
     int32_t* from;            // [heads][B]: listed rows, ascending
     int32_t* to;              // [heads][B]: the places they move to, ascending
+    uint8_t* stays;           // [heads][stays_stride]: a bit a row below t - w that keeps its place (clusters of evict_select)
+    size_t stays_stride;
     int row_chunks;           // d / 8
     int slice;                // evict_select_long: keys that shared memory holds per CTA; 0: read again each round
 };
@@ -352,14 +354,37 @@ __host__ __device__ constexpr int batch_rows(int loads) {
 }
 
 // parts + 1 blocks per head: the first copies the listed rows below t, then the window; the others
-// share the rest of the list.
+// share the rest of the list, and (fill) first write what evict_select left of src and acc_out: rows
+// that keep their places, and -1 past the new length.
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move(const EvictArgs a, int parts, int chunk) {
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move(const EvictArgs a, int parts, int chunk, bool fill) {
     constexpr int kWarps = kMoveThreads / 32, kBatch = batch_rows<D>(kMoveLoads);
     ptx::grid_dependency_wait();
     const int head = blockIdx.x / (parts + 1), part = blockIdx.x % (parts + 1), warp = threadIdx.x >> 5;
     const int4 info = a.info[head];
     const int n = info.x, t = info.y, listed = info.z, early = info.w - 1, w = a.w, round = chunk * kWarps;
+    if (fill && part > 0) {
+        const bool full = n > t, copy = a.acc_out != a.acc;
+        const int last = full ? t : n, split = full ? t - w : n;
+        int32_t* src = a.src ? a.src + (size_t)head * a.B : nullptr;
+        const int first = ((part - 1) * kMoveThreads + threadIdx.x) * 4, step = parts * kMoveThreads * 4;
+        for (int j = first; j < split && (src || copy); j += step) {   // four rows: they lie in one page
+            const int here = min(4, split - j);
+            const uint32_t bits = full ? a.stays[(size_t)head * a.stays_stride + j / 8] >> (j & 4) : 15u;
+            const long long row = copy ? a.c.row(head, j) : -1;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row >= 0) x = *(const float4*)(a.acc + row);
+            const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i >= here || !(bits >> i & 1)) continue;
+                if (src) src[j + i] = j + i;
+                if (row >= 0) a.acc_out[row + i] = v[i];
+            }
+        }
+        if (src)
+            for (int j = last + (part - 1) * kMoveThreads + threadIdx.x; j < a.B; j += parts * kMoveThreads) src[j] = -1;
+    }
     if (early < 0) return;
     const int32_t* from = a.from + (size_t)head * a.B;
     const int32_t* to = a.to + (size_t)head * a.B;
@@ -380,8 +405,13 @@ template <int C>
 struct PickShared {
     __align__(16) uint32_t hist[4][kBins];           // of this CTA's keys, a digit a round
     __align__(16) uint32_t all[2][C > 1 ? C : 1][kBins];   // every CTA's, of the cluster
-    unsigned long long scan[C][kMaxWarps];           // every warp's packed totals for the lists
-    int from[kFew], to[kFew];                        // listed rows, where they are copied here
+    unsigned long long warp_scan[kMaxWarps];         // packed counts: a warp's, then those before it
+    unsigned long long cta_scan[C];                  // every CTA's
+    uint32_t T;                                      // what warp 0 found in the last round
+    int above;
+    bool exact;
+    int from[kFew], to[kFew];                        // listed rows, where they are copied here;
+    long long to_row[kFew];                          // where the places lie in the pool;
     long long row[kFew];                             // rows [t - w, n): where they lie (-1: no page),
     float weight[kFew];                              // and their weights
 };
@@ -391,6 +421,16 @@ struct PickShared {
 __device__ __forceinline__ unsigned long long pack4(int gt_low, int eq_low, int gt_high, int eq_high) {
     return (unsigned long long)gt_low | (unsigned long long)eq_low << 16 | (unsigned long long)gt_high << 32 |
            (unsigned long long)eq_high << 48;
+}
+
+__device__ __forceinline__ unsigned long long warp_inclusive(unsigned long long x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
 }
 
 template <int C, int kPer, int kThreads = kMaxThreads, int kCtas = 1>
@@ -408,52 +448,51 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
     if (C > 1) cluster_arrive();                     // this thread has read lens
     const int split = full ? t - w : n;              // rows below keep their places, or are replaced
     int32_t* src = a.src ? a.src + (size_t)head * a.B : nullptr;
-
+    const bool fill = C == 1;                        // (a cluster leaves it to evict_move)
     // With few rows past t - w, all that can move are fetched while the rest is worked out.
     const bool here = C == 1 && full && n - split <= kFew;
-    const int d_chunks = a.row_chunks;               // 16-byte chunks of a row of keys (then as many of values)
-    if (here) {
-        for (int r = tid; r < n - split; r += threads) {
-            const long long row = a.c.row(head, split + r);
-            sh.row[r] = row;
-            sh.weight[r] = row >= 0 ? a.acc[row] : 0.f;
-        }
-        for (int r = warp; r < n - split; r += warps) {   // a warp a row
-            const long long row = a.c.row(head, split + r);
-            if (row < 0 || lane >= 2 * d_chunks) continue;
-            const uint4* from = (lane < d_chunks ? a.k_pages : a.v_pages) + row * d_chunks + (lane & (d_chunks - 1));
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                             ptx::smem_u32((uint4*)keys + r * 2 * d_chunks + lane)),
-                         "l"(from)
-                         : "memory");
-        }
-    }
 
-    // rows [j0, j0 + kPer) are this thread's. A key is the weight's bits plus one; 0: no candidate.
+    // ---- rows [j0, j0 + kPer) are this thread's. A key is the weight's bits plus one; 0: no candidate.
     const int j0 = (rank * threads + tid) * kPer;
     uint32_t key[kPer];
-    const bool copy = a.acc_out != a.acc;
-    if (copy || full) {
+    if (full || fill) {
         const int32_t* table = a.c.table + (size_t)head * a.c.max_pages;
         float4 x[kPer / 4];
-        size_t row[kPer / 4];
-        bool there[kPer / 4];
+        long long row[kPer / 4];
 #pragma unroll
         for (int q = 0; q < kPer / 4; ++q) {
             const int j = j0 + 4 * q;                // four rows lie in one page
             const int page = j < n ? table[j >> a.c.page_shift] : -1;
-            there[q] = page >= 0 && page < a.c.num_pages;
-            row[q] = ((size_t)max(page, 0) << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
+            row[q] = page < 0 || page >= a.c.num_pages
+                         ? -1 : ((long long)page << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
         }
+        // of the rows that may move, this warp's: r = warp + warps * lane
+        const int r_mine = warp + warps * lane;
+        const long long r_row = here && r_mine < n - split ? a.c.row(head, split + r_mine) : -1;
 #pragma unroll
-        for (int q = 0; q < kPer / 4; ++q) x[q] = there[q] ? *(const float4*)(a.acc + row[q]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = 0; q < kPer / 4; ++q) x[q] = row[q] >= 0 ? *(const float4*)(a.acc + row[q]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (here) {
+            const int chunks = a.row_chunks;         // 16-byte chunks of a row of keys (then as many of values)
+            if (r_mine < n - split) {
+                sh.row[r_mine] = r_row;
+                if (r_row >= 0)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(&sh.weight[r_mine])), "l"(a.acc + r_row) : "memory");
+            }
+            const uint4* pool = (lane < chunks ? a.k_pages : a.v_pages) + (lane & (chunks - 1));
+            for (int r = warp, i = 0; r < n - split; r += warps, ++i) {
+                const long long from = __shfl_sync(0xffffffffu, r_row, i);
+                if (from >= 0 && lane < 2 * chunks)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     ptx::smem_u32((uint4*)keys + r * 2 * chunks + lane)), "l"(pool + from * chunks) : "memory");
+            }
+        }
 #pragma unroll
         for (int q = 0; q < kPer / 4; ++q) {
             const float v[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
             const int j = j0 + 4 * q;
 #pragma unroll
             for (int i = 0; i < 4; ++i) key[4 * q + i] = key_of(v[i]) + 1;
-            if (there[q] && copy) {
+            if (fill && row[q] >= 0 && a.acc_out != a.acc) {
                 if (j + 4 <= split) {
                     *(float4*)(a.acc_out + row[q]) = x[q];
                 } else {
@@ -464,10 +503,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
             }
         }
     }
-    if (src) {
-        // rows that stay (others overwrite theirs when they move), and what lies past the new length
+    if (fill && src) {
+        // rows that stay (those that move write theirs later), and what lies past the new length
         const int last = full ? t : n;
-        for (int i = rank * threads + tid; i < a.B; i += C * threads) {
+        for (int i = tid; i < a.B; i += threads) {
             if (i < split) src[i] = i;
             else if (i >= last) src[i] = -1;
         }
@@ -517,35 +556,43 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
             }
             sync_all<C>();
         }
-        // lane x: digits 255 - 8 x down to 248 - 8 x; every warp finds the same
-        int bin[8] = {};
+        if (warp == 0) {
+            // lane x: digits 255 - 8 x down to 248 - 8 x
+            int bin[8] = {};
 #pragma unroll
-        for (int x = 0; x < C; ++x) {
-            const uint4* from = (const uint4*)((C > 1 ? sh.all[round & 1][x] : hist) + kBins - 8 - 8 * lane);
-            const uint4 lo = from[0], hi = from[1];
-            bin[0] += hi.w, bin[1] += hi.z, bin[2] += hi.y, bin[3] += hi.x;
-            bin[4] += lo.w, bin[5] += lo.z, bin[6] += lo.y, bin[7] += lo.x;
-        }
-        int inc = ((bin[0] + bin[1]) + (bin[2] + bin[3])) + ((bin[4] + bin[5]) + (bin[6] + bin[7]));
-        const int sum = inc;
+            for (int x = 0; x < C; ++x) {
+                const uint4* from = (const uint4*)((C > 1 ? sh.all[round & 1][x] : hist) + kBins - 8 - 8 * lane);
+                const uint4 lo = from[0], hi = from[1];
+                bin[0] += hi.w, bin[1] += hi.z, bin[2] += hi.y, bin[3] += hi.x;
+                bin[4] += lo.w, bin[5] += lo.z, bin[6] += lo.y, bin[7] += lo.x;
+            }
+            int inc = ((bin[0] + bin[1]) + (bin[2] + bin[3])) + ((bin[4] + bin[5]) + (bin[6] + bin[7]));
+            const int sum = inc;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-        }
-        const int want = kk - above;                 // the want-th key from the top is T
-        const int owner = __ffs(__ballot_sync(0xffffffffu, inc >= want)) - 1;   // there is one: more than kk keys
-        int before = inc - sum, digit = 255 - 8 * lane, count = 0;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const int want = kk - above;             // the want-th key from the top is T
+            if (inc - sum < want && want <= inc) {   // one lane: there are more than kk keys
+                int before = inc - sum, digit = 255 - 8 * lane, count = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            count = bin[i];
-            if (before + count >= want) break;
-            before += count;
-            --digit;
+                for (int i = 0; i < 8; ++i) {
+                    count = bin[i];
+                    if (before + count >= want) break;
+                    before += count;
+                    --digit;
+                }
+                sh.T = T | (uint32_t)digit << shift;
+                sh.above = above + before;
+                sh.exact = before + count == want;
+            }
         }
-        T |= (uint32_t)__shfl_sync(0xffffffffu, digit, owner) << shift;
-        above += __shfl_sync(0xffffffffu, before, owner);
-        exact = above + __shfl_sync(0xffffffffu, count, owner) == kk;
+        __syncthreads();
+        T = sh.T;
+        above = sh.above;
+        exact = sh.exact;
+        // (warp 0 writes them again only after the next round's barrier)
     }
     // rows whose key is T that stay, lowest first; none is needed where just kk keys reach T
     const int need_eq = exact ? 0 : kk - above;
@@ -557,43 +604,35 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
     }
     if (exact) eqm = 0;
 
-    // ---- places in the lists
+    // ---- places in the lists: counts before this thread's rows
     const unsigned long long mine = pack4(__popc(gt & low), __popc(eqm & low), __popc(gt & ~low), __popc(eqm & ~low));
-    unsigned long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-    }
-    const unsigned long long whole = __shfl_sync(0xffffffffu, inc, 31);
-    if (C > 1) {
-        if (lane < C) *cg::this_cluster().map_shared_rank(&sh.scan[rank][warp], lane) = whole;
-    } else if (lane == 0) {
-        sh.scan[0][warp] = whole;
+    unsigned long long before = warp_inclusive(mine) - mine;
+    if (lane == 31) sh.warp_scan[warp] = before + mine;
+    __syncthreads();
+    if (warp == 0) {
+        const unsigned long long v = lane < warps ? sh.warp_scan[lane] : 0ull, inc = warp_inclusive(v);
+        if (lane < warps) sh.warp_scan[lane] = inc - v;
+        const unsigned long long all = __shfl_sync(0xffffffffu, inc, 31);
+        if (C > 1) {
+            if (lane < C) *cg::this_cluster().map_shared_rank(&sh.cta_scan[rank], lane) = all;
+        } else if (lane == 0) {
+            sh.cta_scan[0] = all;
+        }
     }
     sync_all<C>();
-    int b_gt_low = 0, b_eq_low = 0, b_gt_high = 0, b_eq_high = 0, all_gt_high = 0, all_eq_low = 0, all_eq_high = 0;
+    before += sh.warp_scan[warp];
+    // 16 bits hold a CTA's counts, not a cluster's
+    int b_gt_low = (int)(before & 0xFFFF), b_eq_low = (int)(before >> 16 & 0xFFFF), b_gt_high = (int)(before >> 32 & 0xFFFF),
+        b_eq_high = (int)(before >> 48), all_eq_low = 0, all_gt_high = 0, all_eq_high = 0;
 #pragma unroll
     for (int x = 0; x < C; ++x) {
-        const unsigned long long v = lane < warps ? sh.scan[x][lane] : 0ull;
-        const bool before = x < rank || (x == rank && lane < warp);
+        const unsigned long long v = sh.cta_scan[x];
         const int gl = (int)(v & 0xFFFF), el = (int)(v >> 16 & 0xFFFF), gh = (int)(v >> 32 & 0xFFFF), eh = (int)(v >> 48);
-        b_gt_low += before ? gl : 0;
-        b_eq_low += before ? el : 0;
-        b_gt_high += before ? gh : 0;
-        b_eq_high += before ? eh : 0;
+        if (x < rank) b_gt_low += gl, b_eq_low += el, b_gt_high += gh, b_eq_high += eh;
         all_eq_low += el;
         all_gt_high += gh;
         all_eq_high += eh;
     }
-    const unsigned long long excl = inc - mine;      // of the lanes before this one
-    b_gt_low = __reduce_add_sync(0xffffffffu, b_gt_low) + (int)(excl & 0xFFFF);
-    b_eq_low = __reduce_add_sync(0xffffffffu, b_eq_low) + (int)(excl >> 16 & 0xFFFF);
-    b_gt_high = __reduce_add_sync(0xffffffffu, b_gt_high) + (int)(excl >> 32 & 0xFFFF);
-    b_eq_high = __reduce_add_sync(0xffffffffu, b_eq_high) + (int)(excl >> 48);
-    all_eq_low = __reduce_add_sync(0xffffffffu, all_eq_low);
-    all_gt_high = __reduce_add_sync(0xffffffffu, all_gt_high);
-    all_eq_high = __reduce_add_sync(0xffffffffu, all_eq_high);
     // equal rows stay from the lowest on, and the low ones come first
     const int listed = all_gt_high + min(all_eq_low + all_eq_high, need_eq) - min(all_eq_low, need_eq);
     const int eq = b_eq_low + b_eq_high, room = max(0, need_eq - eq);    // equal rows before; of this thread's, that stay
@@ -607,14 +646,26 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
     int at = max(0, min(j0, n - w) - s) - kept_low;
     for (uint32_t m = cand & low & ~kept; m; m &= m - 1, ++at) {
         const int j = j0 + __ffs(m) - 1;
-        if (here) sh.to[at] = j;
-        else if (KVP_CHECK(at >= 0 && at < a.B, 701, head, at)) to[at] = j;
+        if (here) {
+            sh.to[at] = j;
+            sh.to_row[at] = a.c.row(head, j);
+        } else if (KVP_CHECK(at >= 0 && at < a.B, 701, head, at)) {
+            to[at] = j;
+        }
     }
     at = kept_high;
     for (uint32_t m = kept & ~low; m; m &= m - 1, ++at) {
         const int j = j0 + __ffs(m) - 1;
         if (here) sh.from[at] = j;
         else if (KVP_CHECK(at < a.B, 702, head, at)) from[at] = j;
+    }
+    if (!fill) {
+        // evict_move fills in src and acc_out of the rows that stay: a bit each
+        const uint32_t stays = low & (kept | first_bits(s));
+        if (j0 < split) {
+            if (kPer == 16) ((uint16_t*)a.stays)[((size_t)head * a.stays_stride + j0 / 8) / 2] = (uint16_t)stays;
+            else a.stays[(size_t)head * a.stays_stride + j0 / 8] = (uint8_t)stays;
+        }
     }
     if (j0 <= t && t < j0 + kPer)                    // row t is this thread's
         a.info[head] = make_int4(n, t, listed, here ? 0 : 1 + kept_high + __popc(kept & ~low & first_bits(t)));
@@ -624,17 +675,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
         // a warp a row: the listed ones, then the window; all that is read is in shared memory
+        const int chunks = a.row_chunks;
+        uint4* pool = (lane < chunks ? a.k_pages : a.v_pages) + (lane & (chunks - 1));
         for (int i = warp; i < listed + w; i += warps) {
             const bool is_listed = i < listed;
             const int r = is_listed ? sh.from[i] - split : n - w - split + i - listed;     // source
             const int place = is_listed ? sh.to[i] : split + i - listed;
-            const long long to = is_listed ? a.c.row(head, place) : sh.row[i - listed];
+            const long long to_row = is_listed ? sh.to_row[i] : sh.row[i - listed];
             if (src && lane == 0) src[place] = split + r;
-            if (sh.row[r] < 0 || to < 0) continue;
-            if (!KVP_CHECK(to < ((long long)a.c.num_pages << a.c.page_shift), 704, head, place)) continue;
-            if (lane < 2 * d_chunks)
-                ((lane < d_chunks ? a.k_pages : a.v_pages) + to * d_chunks)[lane & (d_chunks - 1)] = ((const uint4*)keys)[r * 2 * d_chunks + lane];
-            if (lane == 0) a.acc_out[to] = sh.weight[r];
+            if (sh.row[r] < 0 || to_row < 0) continue;
+            if (!KVP_CHECK(to_row < ((long long)a.c.num_pages << a.c.page_shift), 704, head, place)) continue;
+            if (lane < 2 * chunks) pool[to_row * chunks] = ((const uint4*)keys)[r * 2 * chunks + lane];
+            if (lane == 0) a.acc_out[to_row] = sh.weight[r];
         }
     }
 }
@@ -663,9 +715,13 @@ cudaError_t launch_heads(void (*kernel)(const EvictArgs), const EvictArgs& a, in
 
 }  // namespace
 
+// Bytes of a head's bits, a multiple of two (evict_select writes 16 of them at a time).
+static size_t stays_stride(const kvp_cache_shape& s) { return (size_t)s.max_pages * s.page_size / 8; }
+
 size_t evict_workspace_bytes(const kvp_cache_shape& s, const kvp_evict& e) {
     const size_t heads = (size_t)s.batch * s.hkv;
-    return align256(heads * sizeof(int4)) + 2 * align256(heads * e.budget * sizeof(int32_t));
+    return align256(heads * sizeof(int4)) + 2 * align256(heads * e.budget * sizeof(int32_t)) +
+           align256(heads * stays_stride(s));
 }
 
 cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int32_t* budgets,
@@ -689,6 +745,8 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
     a.info = (int4*)ws;
     a.from = (int32_t*)(ws + align256((size_t)heads * sizeof(int4)));
     a.to = (int32_t*)(ws + align256((size_t)heads * sizeof(int4)) + align256((size_t)heads * e.budget * 4));
+    a.stays = (uint8_t*)(ws + align256((size_t)heads * sizeof(int4)) + 2 * align256((size_t)heads * e.budget * 4));
+    a.stays_stride = stays_stride(s);
     a.slice = 0;
     a.row_chunks = s.head_dim / 8;
     // CTAs per head: 8 where the heads alone would leave most SMs idle and rows are many
@@ -696,6 +754,7 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
     const int C = cap > 4096 && (heads * 2 < sms || cap > kMaxThreads * kPerMost) ? 8 : 1;
     const int slice = (cap + C - 1) / C;
     cudaError_t err;
+    bool fill = false;
     if (slice <= kMaxThreads * kPerMost) {
         // a cluster, whose CTAs have an SM each: 8 keys a thread, 16 once that takes more than 1024
         // threads; else 16, for several CTAs an SM
@@ -703,6 +762,7 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
         const int threads = std::max(64, (slice + per * 32 - 1) / (per * 32) * 32);
         if (C == 8) {
             err = launch_heads(per == 8 ? evict_select<8, 8> : evict_select<8, kPerMost>, a, C, threads, 0, st);
+            fill = true;
         } else {
             err = launch_heads(per == 8 ? evict_select<1, 8, kManyThreads, 3> : evict_select<1, kPerMost>, a, C, threads, (size_t)kFew * s.head_dim * 4, st);
         }
@@ -719,9 +779,11 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
     const int warps = sms * kMoveCtas * (kMoveThreads / 32), batch = s.head_dim == 128 ? batch_rows<128>(kMoveLoads) : batch_rows<64>(kMoveLoads);
     const int chunk = (int)std::min<long long>(32, std::max<long long>(batch, (long long)heads * most / warps / batch * batch));
     const int round = chunk * (kMoveThreads / 32);
-    const int parts = std::max(1, std::min((most + round - 1) / round, sms * kMoveCtas / heads - 1));
-    return s.head_dim == 128 ? launch_dependent(evict_move<128>, heads * (parts + 1), kMoveThreads, 0, st, a, parts, chunk)
-                             : launch_dependent(evict_move<64>, heads * (parts + 1), kMoveThreads, 0, st, a, parts, chunk);
+    const int filled = fill ? std::min(e.budget, cap) : 0;
+    const int want = std::max((most + round - 1) / round, (filled + kMoveThreads * 4 - 1) / (kMoveThreads * 4));
+    const int parts = std::max(1, std::min(want, sms * kMoveCtas / heads - 1));
+    return s.head_dim == 128 ? launch_dependent(evict_move<128>, heads * (parts + 1), kMoveThreads, 0, st, a, parts, chunk, fill)
+                             : launch_dependent(evict_move<64>, heads * (parts + 1), kMoveThreads, 0, st, a, parts, chunk, fill);
 }
 
 #ifdef KVP_CHECKS
