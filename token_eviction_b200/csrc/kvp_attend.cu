@@ -556,35 +556,48 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
             __syncthreads();
             const int slot = 2 * cta + (segment ? 1 : 0);
             const bool whole = m.valid_flags & kWhole;
-            for (int e = tid; e < nq * D; e += kThreads) {
-                const int row = e / D, col = e % D;
-                float top = kLowest;
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) top = fmaxf(top, sh_stat[x][row].x);
-                float l = 0.f, val = 0.f;
+            // a warp every kWarps-th query head, a lane kCols columns
+            constexpr int kCols = D / 32;
+            for (int row = warp; row < nq; row += kWarps) {
+                float2 st[kWarps];
+                float top = kLowest, l = 0.f, val[kCols] = {};
 #pragma unroll
                 for (int x = 0; x < kWarps; ++x) {
-                    const float2 st = sh_stat[x][row];
-                    const float f = ptx::ex2(st.x - top);
-                    l += f * st.y;
-                    val += f * ((const float*)(ring + (size_t)(x * kStages + stage) * S::kStage))[row * D + (col ^ ((row & 3) << 3))];
+                    st[x] = sh_stat[x][row];
+                    top = fmaxf(top, st[x].x);
+                }
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) {
+                    const float f = ptx::ex2(st[x].x - top);
+                    l += f * st[x].y;
+                    const float* from = (const float*)(ring + (size_t)(x * kStages + stage) * S::kStage) + row * D +
+                                        ((lane * kCols) ^ ((row & 3) << 3));
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) val[c] += f * from[c];
                 }
                 top -= Pair<T>::kBias;         // the sum and the output are 2^kBias larger
                 const size_t query = (size_t)head * a.G + g0 + row;
                 if (whole) {
                     const float inv = l == 0.f ? 0.f : 1.f / l;     // a NaN sum stays one
-                    ((T*)a.out)[query * D + col] = T(val * inv);
-                    if (col == 0) {
+                    uint32_t packed[kCols / 2];
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 2) packed[c / 2] = Pair<T>::pack(val[c] * inv, val[c + 1] * inv);
+#pragma unroll
+                    for (int c = 0; c < kCols / 2; ++c) ((uint32_t*)a.out)[(query * D + lane * kCols) / 2 + c] = packed[c];
+                    if (lane == 0) {
                         const float lse2 = top + log2f(l);          // -inf where l is 0
                         if (a.lse) a.lse[query] = lse2 * kLn2;
                         if (a.lse2) a.lse2[query] = lse2;
                         sh_lse2[row] = l == 0.f ? INFINITY : lse2;
                     }
                 } else {
-                    a.parts[((size_t)slot * a.gq + row) * D + col] = val;
-                    if (col == 0) a.stats[(size_t)slot * a.gq + row] = make_float2(top, l);
+                    float* to = a.parts + ((size_t)slot * a.gq + row) * D + lane * kCols;
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) to[c] = val[c];
+                    if (lane == 0) a.stats[(size_t)slot * a.gq + row] = make_float2(top, l);
                 }
             }
+            __syncthreads();
             if (!whole && tid == 0) {
                 Cut x;
                 const int tile = m.row0 / kTile - (step - seg_step);   // the share's first
@@ -599,7 +612,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
                 x.later = cut(x.c0, T_, parties) < first;
                 a.cuts[slot] = x;
             }
-            __syncthreads();
             if (whole && a.logits && a.ng == 1)
                 add_weights<kThreads>(a, head, 0, a.c.len(head), tid, sh_lse2);
             segment = 1;
