@@ -38,7 +38,7 @@ constexpr int kTile = kWarps * kGroup;            // rows a CTA takes at a time
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxGrid = kPlanGrid * kCtasPerSm;  // the workspace holds parts for as many CTAs
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinPieces = 4;                    // blocks of attend_join that weigh one share
+constexpr int kJoinPieces = 4;                    // blocks of attend_join that weigh one share, at most
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.4028234663852886e38f;  // of a maximum over nothing: finite, so that
                                                     // differences of maxima are never inf - inf
@@ -642,17 +642,17 @@ __device__ __forceinline__ float joined_lse2(const AttendArgs& a, const Cut& p, 
     return m + log2f(l);
 }
 
-// Two kinds of blocks, none with more than one short chain of reads. The first kJoinPieces blocks
-// for every share of a cut unit (with acc): add its rows' weights. Then `rows` blocks for every CTA
-// of attend_split, one a query head: join the outputs of the units whose first share it had.
+// Two kinds of blocks, none with more than one short chain of reads. The first, `pieces` for every
+// share of a cut unit (with acc), add its rows' weights. Then `rows` blocks for every CTA of
+// attend_split, one a query head, join the outputs of the units whose first share it had.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendArgs a, int weighers, int rows) {
+__global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendArgs a, int weighers, int pieces, int rows) {
     __shared__ float sh_lse2[16];
     ptx::grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if ((int)blockIdx.x < weighers) {
-        const Cut p = a.cuts[blockIdx.x / kJoinPieces];
-        const int piece = blockIdx.x % kJoinPieces;
+        const Cut p = a.cuts[blockIdx.x / pieces];
+        const int piece = blockIdx.x % pieces;
         constexpr int kRound = kJoinThreads * 4;
         const int last = min(p.len, (p.tile + p.count) * kTile), first = p.tile * kTile + piece * kRound;
         if (p.unit < 0 || first >= last) return;
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendArgs 
             if (lane == 0) sh_lse2[row] = x == -INFINITY ? INFINITY : x;
         }
         __syncthreads();
-        for (int j = first; j < last; j += kJoinPieces * kRound)
+        for (int j = first; j < last; j += pieces * kRound)
             add_weights<kJoinThreads>(a, p.head, j, min(last, j + kRound), tid, sh_lse2);
         return;
     }
@@ -780,13 +780,18 @@ cudaError_t launch_split(const AttendArgs& a, int grid, cudaStream_t st) {
 }
 
 template <typename T, int D>
-cudaError_t launch_all(const AttendArgs& a, int grid, cudaStream_t st) {
+cudaError_t launch_all(const AttendArgs& a, cudaStream_t st) {
     constexpr int kStages = D == 128 ? 3 : 6;
+    // as many CTAs as are resident at once, but no more than there can be tiles
+    const long long most = (long long)a.c.heads * a.ng * ((a.c.cap() + kTile - 1) / kTile);
+    const int grid = (int)std::min<long long>(most, std::min(num_sms(), kPlanGrid) * kCtasPerSm);
     cudaError_t e = a.gq == 16 ? launch_split<T, D, true, kStages>(a, grid, st)
-                                     : launch_split<T, D, false, kStages>(a, grid, st);
+                               : launch_split<T, D, false, kStages>(a, grid, st);
     if (e != cudaSuccess) return e;
-    const int weighers = a.logits && a.ng == 1 ? 2 * grid * kJoinPieces : 0, rows = std::min(a.G, a.gq);
-    e = launch_dependent(attend_join<T, D>, weighers + grid * rows, kJoinThreads, 0, st, a, weighers, rows);
+    const long long share = (most + grid - 1) / grid * kTile;       // rows of a share, at most
+    const int pieces = (int)std::min<long long>(kJoinPieces, (share + kJoinThreads * 4 - 1) / (kJoinThreads * 4));
+    const int weighers = a.logits && a.ng == 1 ? 2 * grid * pieces : 0, rows = std::min(a.G, a.gq);
+    e = launch_dependent(attend_join<T, D>, weighers + grid * rows, kJoinThreads, 0, st, a, weighers, pieces, rows);
     if (e != cudaSuccess || !a.lse2) return e;
     const int per = std::max(1, std::min(num_sms() * 8 / a.c.heads, (a.c.cap() + kJoinThreads * 4 - 1) / (kJoinThreads * 4)));
     return launch_dependent(attend_weigh, a.c.heads * per, kJoinThreads, 0, st, a, per);
@@ -818,11 +823,10 @@ cudaError_t launch_attend(const kvp_cache_shape& s, const uint16_t* q, const uin
     a.parts = (float*)(ws + l.parts);
     a.lse2 = acc && l.ng > 1 ? (float*)(ws + l.lse2) : nullptr;
     a.logits = acc ? (float*)(ws + l.logits) : nullptr;
-    const int grid = std::min(num_sms(), kPlanGrid) * kCtasPerSm;
     if (s.dtype == KVP_BF16)
-        return s.head_dim == 128 ? launch_all<__nv_bfloat16, 128>(a, grid, st)
-                                 : launch_all<__nv_bfloat16, 64>(a, grid, st);
-    return s.head_dim == 128 ? launch_all<__half, 128>(a, grid, st) : launch_all<__half, 64>(a, grid, st);
+        return s.head_dim == 128 ? launch_all<__nv_bfloat16, 128>(a, st)
+                                 : launch_all<__nv_bfloat16, 64>(a, st);
+    return s.head_dim == 128 ? launch_all<__half, 128>(a, st) : launch_all<__half, 64>(a, st);
 }
 
 #ifdef KVP_CHECKS
