@@ -323,27 +323,243 @@ struct __align__(16) Meta {
 // kFirst, kLast: of the unit, within this CTA's run; kWhole: the run has all of the unit
 constexpr int kFirst = 32, kLast = 64, kWhole = 128, kValid = 31;
 
-// Elements: T. D: head dimension. kWide: up to 16 query heads a unit, one row each of the MMA's
-// 16; else up to 8, whose weights fill rows 0-7 and the remainders left by rounding them to T
-// rows 8-15: the product with V then carries about twice T's precision, for free, since the
-// MMA has 16 rows anyway.
-constexpr uint32_t kRingAlign = 256;      // rows of 256 bytes: a chunk's bits of an address are free for xor
-
-template <typename T, int D, bool kWide, int kStages>
-struct Split {
+// How 16 rows of keys or values lie in shared memory, and how a warp fetches and reads them. A row's
+// 16-byte chunks are stored xor (row & 7), so that eight rows' same chunk lies in eight bank groups.
+template <int D>
+struct Group16 {
     static constexpr int kRowBytes = D * 2;
     static constexpr int kChunks = D / 8;                       // 16-byte chunks of a row
     static constexpr int kHalf = kGroup * kRowBytes;            // a group's keys (then its values)
     static constexpr int kStage = 2 * kHalf;
-    static constexpr int kQ = kWide ? 16 : 8;                   // query heads a unit
+    static constexpr int kRowsAt = 32 / kChunks;                // rows that one load of the warp covers
+
+    const uint8_t *k, *v, *k_lane, *v_lane;
+    uint32_t dst_lane;       // offset of this lane's first chunk in a stage
+    uint64_t policy;
+
+    __device__ __forceinline__ Group16(const AttendArgs& a) {
+        const int lane = threadIdx.x & 31, chunk = lane % kChunks, lrow = lane / kChunks;   // lrow < kRowsAt <= 4
+        k = (const uint8_t*)a.k;
+        v = (const uint8_t*)a.v;
+        k_lane = k + lrow * kRowBytes + chunk * 16;
+        v_lane = v + lrow * kRowBytes + chunk * 16;
+        dst_lane = lrow * kRowBytes + ((chunk ^ lrow) << 4);
+        policy = ptx::policy_evict_first();   // rows are read once; what L2 holds better is the logits
+    }
+    // Rows [row, row + valid) of the pool into the stage at `stage`, zeros behind them.
+    __device__ __forceinline__ void fetch(uint32_t stage, size_t row, int valid) const {
+        const size_t off = row * kRowBytes;
+        const uint32_t dst = stage + dst_lane;
+        if (valid == kGroup) {
+            const uint8_t *ks = k_lane + off, *vs = v_lane + off;
+#pragma unroll
+            for (int i = 0; i < kGroup / kRowsAt; ++i) {
+                const int r = i * kRowsAt;                 // lrow | r: they share no bits
+                cp16((dst ^ ((r & 7) << 4)) + r * kRowBytes, ks + r * kRowBytes, policy);
+            }
+#pragma unroll
+            for (int i = 0; i < kGroup / kRowsAt; ++i) {
+                const int r = i * kRowsAt;
+                cp16((dst ^ ((r & 7) << 4)) + r * kRowBytes + kHalf, vs + r * kRowBytes, policy);
+            }
+        } else if (valid > 0) {
+            const int lrow = (threadIdx.x & 31) / kChunks;
+#pragma unroll 1
+            for (int r = 0; r < kGroup; r += kRowsAt) {
+                const bool in = lrow + r < valid;
+                const size_t from = in ? off + (size_t)r * kRowBytes : 0;
+                const uint32_t to = (dst ^ ((r & 7) << 4)) + r * kRowBytes;
+                cp16_or_zero(to, (in ? k_lane : k) + from, in);
+                cp16_or_zero(to + kHalf, (in ? v_lane : v) + from, in);
+            }
+        }
+    }
+};
+
+// A warp's running softmax over groups of 16 rows, for up to 16 query heads (kWide), one row each of
+// the MMA's 16; or for up to 8, whose weights fill rows 0-7 and the remainders left by rounding
+// them to T rows 8-15: the product with V then carries about twice T's precision, for free, since
+// the MMA has 16 rows anyway.
+template <typename T, int D, bool kWide>
+struct Running {
+    static constexpr int kNt = D / 8;         // 8-column tiles of the output
+    static constexpr int kR = kWide ? 2 : 1;  // rows of the MMA that are query heads: gid, gid + 8
+    static constexpr int kQ = 8 * kR;
+    float o[kNt][4];
+    float m_run[2], l_run[2];                 // running maximum (log2 units) and sum
+    uint32_t qf[D / 16][2 * kR];
+
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int i = 0; i < kNt; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        m_run[0] = m_run[1] = kLowest;
+        l_run[0] = l_run[1] = 0.f;
+    }
+    // q: the unit's first query head, of nq
+    __device__ __forceinline__ void read_q(const uint16_t* q, int nq) {
+        const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+        const uint32_t* qp = (const uint32_t*)q;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const int at32 = ks * 8 + tig;              // pairs of columns
+            qf[ks][0] = gid < nq ? qp[gid * (D / 2) + at32] : 0u;
+            qf[ks][1] = gid < nq ? qp[gid * (D / 2) + at32 + 4] : 0u;
+            if (kWide) {
+                qf[ks][kR] = gid + 8 < nq ? qp[(gid + 8) * (D / 2) + at32] : 0u;
+                qf[ks][2 * kR - 1] = gid + 8 < nq ? qp[(gid + 8) * (D / 2) + at32 + 4] : 0u;
+            }
+        }
+    }
+    // The group in the stage at `stage`, `valid` > 0 rows of it. put(r, row, x, y): products q . k of
+    // query head gid + 8 r with rows `row` and row + 1.
+    template <typename Put>
+    __device__ __forceinline__ void take(uint32_t stage, int valid, float scale2, Put put) {
+        constexpr int kRowBytes = Group16<D>::kRowBytes;
+        const int lane = threadIdx.x & 31, tig = lane & 3;
+        // a lane's address for ldmatrix: chunk c of its row lies 16 c bytes on, by xor
+        const int k_row = (lane & 7) + ((lane >> 4) & 1) * 8, v_row = (lane & 7) + ((lane >> 3) & 1) * 8;
+        const uint32_t sk = stage + k_row * kRowBytes + ((((lane >> 3) & 1) ^ (k_row & 7)) << 4);
+        const uint32_t sv = stage + Group16<D>::kHalf + v_row * kRowBytes + ((((lane >> 4) & 1) ^ (v_row & 7)) << 4);
+        // logits of 16 rows: two tiles of 8 rows, two chains each
+        float c[2][2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t b0, b1, b2, b3;
+            ldsm4(sk ^ (ks << 5), b0, b1, b2, b3);
+            const uint32_t a1 = kWide ? qf[ks][kR] : 0u, a3 = kWide ? qf[ks][2 * kR - 1] : 0u;
+            Pair<T>::mma(c[ks & 1][0], qf[ks][0], a1, qf[ks][1], a3, b0, b1);
+            Pair<T>::mma(c[ks & 1][1], qf[ks][0], a1, qf[ks][1], a3, b2, b3);
+        }
+        float t[2][2 * kR];                   // [8-row tile][query head gid: 2 cached rows, gid + 8: 2]
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 2 * kR; ++i) t[n][i] = c[0][n][i] + c[1][n][i];
+        if (valid < kGroup) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 2 * kR; ++i)
+                    if (n * 8 + 2 * tig + (i & 1) >= valid) t[n][i] = -INFINITY;
+        }
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            put(r, 2 * tig, t[0][2 * r], t[0][2 * r + 1]);
+            put(r, 2 * tig + 8, t[1][2 * r], t[1][2 * r + 1]);
+        }
+        uint32_t pa[4];                       // the weights as the A operand of P V
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            float mx = fmaxf(fmaxf(t[0][2 * r], t[0][2 * r + 1]), fmaxf(t[1][2 * r], t[1][2 * r + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * scale2;
+            if (__any_sync(0xffffffffu, mx > m_run[r])) {
+                const float m_new = fmaxf(m_run[r], mx), f = ptx::ex2(m_run[r] - m_new);
+                l_run[r] *= f;
+#pragma unroll
+                for (int i = 0; i < kNt; ++i) {
+                    o[i][2 * r] *= f;
+                    o[i][2 * r + 1] *= f;
+                    if (!kWide) {             // rows 8-15 are the same query heads' remainders
+                        o[i][2] *= f;
+                        o[i][3] *= f;
+                    }
+                }
+                m_run[r] = m_new;
+            }
+            const float off = Pair<T>::kBias - m_run[r];
+            const float p0 = ptx::ex2(fmaf(t[0][2 * r], scale2, off)), p1 = ptx::ex2(fmaf(t[0][2 * r + 1], scale2, off));
+            const float p2 = ptx::ex2(fmaf(t[1][2 * r], scale2, off)), p3 = ptx::ex2(fmaf(t[1][2 * r + 1], scale2, off));
+            l_run[r] += (p0 + p1) + (p2 + p3);
+            pa[r] = Pair<T>::pack(p0, p1);
+            pa[r + 2] = Pair<T>::pack(p2, p3);
+            if (!kWide) {
+                const float2 h0 = Pair<T>::unpack(pa[0]), h1 = Pair<T>::unpack(pa[2]);
+                pa[1] = Pair<T>::pack(p0 - h0.x, p1 - h0.y);
+                pa[3] = Pair<T>::pack(p2 - h1.x, p3 - h1.y);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kNt; i += 2) {
+            uint32_t b0, b1, b2, b3;
+            ldsm4t(sv ^ (i << 4), b0, b1, b2, b3);
+            Pair<T>::mma(o[i], pa[0], pa[1], pa[2], pa[3], b0, b1);
+            Pair<T>::mma(o[i + 1], pa[0], pa[1], pa[2], pa[3], b2, b3);
+        }
+    }
+    // This warp's part: unnormalised output [kQ][D] (columns xor part_swizzle(row)), maximum and sum [kQ].
+    __device__ __forceinline__ void put_part(float* part, float2* stat) const {
+        const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            float l = l_run[r];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            const int row = gid + 8 * r;
+            if (tig == 0) stat[row] = make_float2(m_run[r], l);
+#pragma unroll
+            for (int i = 0; i < kNt; ++i) {
+                const float x = kWide ? o[i][2 * r] : o[i][0] + o[i][2];
+                const float y = kWide ? o[i][2 * r + 1] : o[i][1] + o[i][3];
+                *(float2*)(part + row * D + ((i * 8 + 2 * tig) ^ part_swizzle(row))) = make_float2(x, y);
+            }
+        }
+    }
+    static __device__ __forceinline__ int part_swizzle(int row) { return (row & 3) << 3; }
+};
+
+// A warp adds up kParts parts of one query head: columns [lane D / 32, ...) of it in val; the maximum
+// and the sum returned. part(x): its output; stat(x): its maximum and sum.
+template <int D, int kParts, typename PartOf, typename StatOf>
+__device__ __forceinline__ float2 add_parts(float (&val)[D / 32], PartOf part, StatOf stat) {
+    float2 st[kParts];
+    float top = kLowest, l = 0.f;
+#pragma unroll
+    for (int x = 0; x < kParts; ++x) {
+        st[x] = stat(x);
+        top = fmaxf(top, st[x].x);
+    }
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) val[c] = 0.f;
+#pragma unroll
+    for (int x = 0; x < kParts; ++x) {
+        const float f = ptx::ex2(st[x].x - top);
+        const float* from = part(x);
+        l += f * st[x].y;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) val[c] += f * from[c];
+    }
+    return make_float2(top, l);
+}
+
+// A finished query head: its output (a lane D / 32 columns) and, by lane 0, its log-sum-exp. Returns
+// log2 of the sum, +inf where there is none.
+template <typename T, int D>
+__device__ __forceinline__ float put_output(const AttendArgs& a, size_t query, const float (&val)[D / 32], float2 st) {
+    const int lane = threadIdx.x & 31;
+    const float inv = st.y == 0.f ? 0.f : 1.f / st.y;               // a NaN sum stays one
+#pragma unroll
+    for (int c = 0; c < D / 32; c += 2)
+        ((uint32_t*)a.out)[(query * D + lane * (D / 32) + c) / 2] = Pair<T>::pack(val[c] * inv, val[c + 1] * inv);
+    // the sum and the output are 2^kBias larger
+    const float lse2 = st.x - Pair<T>::kBias + log2f(st.y);         // -inf where the sum is 0
+    if (lane == 0 && a.lse) a.lse[query] = lse2 * kLn2;
+    if (lane == 0 && a.lse2) a.lse2[query] = lse2;
+    return st.y == 0.f ? INFINITY : lse2;
+}
+
+constexpr uint32_t kRingAlign = 256;      // rows of 256 bytes: a chunk's bits of an address are free for xor
+
+template <typename T, int D, bool kWide, int kStages>
+struct Split {
+    static constexpr int kStage = Group16<D>::kStage;
     static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage + kRingAlign;
-    static_assert(kQ * D * 4 <= kStage, "a warp's part is joined in the stage it has consumed");
+    static_assert(Running<T, D, kWide>::kQ * D * 4 <= kStage, "a warp's part is joined in the stage it has consumed");
 };
 
 template <typename T, int D, bool kWide, int kStages>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const AttendArgs a) {
-    using S = Split<T, D, kWide, kStages>;
-    constexpr int kRowBytes = S::kRowBytes, kQ = S::kQ;
+    constexpr int kStage = Group16<D>::kStage, kQ = Running<T, D, kWide>::kQ;
     extern __shared__ __align__(16) uint8_t raw[];
     uint8_t* const ring = raw + (-ptx::smem_u32(raw) & (kRingAlign - 1));
     __shared__ long long warp_sums[kWarps];
@@ -352,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
     __shared__ float2 sh_stat[kWarps][kQ];
     __shared__ float sh_lse2[kQ];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int gid = lane >> 2, tig = lane & 3;
+    const int gid = lane >> 2;
     const int grid = gridDim.x, cta = blockIdx.x;
 
     ptx::grid_dependency_wait();
@@ -372,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
     // ---- the issuing side: the walk is one tile ahead of its loads, so that its page is at hand
     Walk w;
     w.begin(a.c, a.ng, at);
-    const uint32_t my_ring = ptx::smem_u32(ring) + warp * kStages * S::kStage;
+    const uint32_t my_ring = ptx::smem_u32(ring) + warp * kStages * kStage;
     // pages of the walk's unit, a lane each: of this warp's groups in tiles [page_base, page_base + 32)
     int page_base = 0, pages = -1;
     auto load_pages = [&]() {
@@ -386,16 +602,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
     };
     load_pages();
     int issued = 0, fill = 0;                // groups issued; the stage the next one goes to
-    const uint64_t stream = ptx::policy_evict_first();   // rows are read once; what L2 holds better is the logits
     bool fresh = true;                       // the walk's tile is the run's first of its unit
     bool begins = w.tile == 0;               // and the unit's first
-    // lanes of a load: kChunks lanes to a row, kRowsAt rows at a time. A row's chunks are stored
-    // xor (row & 7), so that eight rows' same chunk lies in eight bank groups.
-    constexpr int kRowsAt = 32 / S::kChunks;
-    const int chunk = lane % S::kChunks, lrow = lane / S::kChunks;
-    const uint8_t* k_lane = (const uint8_t*)a.k + lrow * kRowBytes + chunk * 16;
-    const uint8_t* v_lane = (const uint8_t*)a.v + lrow * kRowBytes + chunk * 16;
-    const uint32_t dst_lane = my_ring + lrow * kRowBytes + ((chunk ^ lrow) << 4);   // lrow < kRowsAt <= 4
+    const Group16<D> group(a);
     const int page_mask = (1 << a.c.page_shift) - 1;
     auto issue = [&]() {
         if (issued < steps) {
@@ -412,30 +621,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
                                 (ends && begins ? kWhole : 0);
                 meta[warp][fill] = m;
             }
-            const size_t off = (((size_t)page << a.c.page_shift) + (row0 & page_mask)) * kRowBytes;
-            const uint32_t dst = dst_lane + fill * S::kStage;
-            if (valid == kGroup) {
-                const uint8_t *ks = k_lane + off, *vs = v_lane + off;
-#pragma unroll
-                for (int i = 0; i < kGroup / kRowsAt; ++i) {
-                    const int r = i * kRowsAt;                 // lrow | r: they share no bits
-                    cp16((dst ^ ((r & 7) << 4)) + r * kRowBytes, ks + r * kRowBytes, stream);
-                }
-#pragma unroll
-                for (int i = 0; i < kGroup / kRowsAt; ++i) {
-                    const int r = i * kRowsAt;
-                    cp16((dst ^ ((r & 7) << 4)) + r * kRowBytes + S::kHalf, vs + r * kRowBytes, stream);
-                }
-            } else if (valid > 0) {                            // zeros for the rows that are not there
-#pragma unroll 1
-                for (int r = 0; r < kGroup; r += kRowsAt) {
-                    const bool in = lrow + r < valid;
-                    const size_t from = in ? off + (size_t)r * kRowBytes : 0;
-                    const uint32_t to = (dst ^ ((r & 7) << 4)) + r * kRowBytes;
-                    cp16_or_zero(to, (in ? k_lane : (const uint8_t*)a.k) + from, in);
-                    cp16_or_zero(to + S::kHalf, (in ? v_lane : (const uint8_t*)a.v) + from, in);
-                }
-            }
+            group.fetch(my_ring + fill * kStage, ((size_t)page << a.c.page_shift) + (row0 & page_mask), valid);
             fill = fill == kStages - 1 ? 0 : fill + 1;
             ++issued;
             if (issued < steps) {
@@ -452,18 +638,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
     for (int i = 0; i < kStages - 1; ++i) issue();
 
     // ---- the consuming side
-    constexpr int kNt = D / 8;                // 8-column tiles of the output
-    constexpr int kR = kWide ? 2 : 1;         // rows of the MMA that are query heads: gid, gid + 8
-    float o[kNt][4];
-    float m_run[2], l_run[2];                 // running maximum (log2 units) and sum
-    uint32_t qf[D / 16][kWide ? 4 : 2];
-    // a lane's address for ldmatrix within a stage: chunk c of its row lies 16 c bytes on, by xor
-    const int k_row = (lane & 7) + ((lane >> 4) & 1) * 8, v_row = (lane & 7) + ((lane >> 3) & 1) * 8;
-    const uint32_t k_at = my_ring + k_row * kRowBytes + ((((lane >> 3) & 1) ^ (k_row & 7)) << 4);
-    const uint32_t v_at = my_ring + S::kHalf + v_row * kRowBytes + ((((lane >> 4) & 1) ^ (v_row & 7)) << 4);
+    Running<T, D, kWide> run;
     int segment = 0, seg_step = 0;            // units begun before this one; the step that began it
     int head = 0, g0 = 0, nq = 0;             // the unit's head, first query head and how many
-    float* lp = nullptr;                      // logits of query head gid, row 2 tig of the head
+    float* lp = nullptr;                      // logits of query head gid of the unit
     const size_t lp_row = (size_t)a.c.cap();
 
     int stage = 0;
@@ -478,156 +656,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
             head = m.head;
             g0 = m.sub * a.gq;
             nq = min(a.gq, a.G - g0);
-#pragma unroll
-            for (int i = 0; i < kNt; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-            m_run[0] = m_run[1] = kLowest;
-            l_run[0] = l_run[1] = 0.f;
-            const uint32_t* qp = (const uint32_t*)(a.q + ((size_t)head * a.G + g0) * D);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const int at32 = ks * 8 + tig;          // pairs of columns
-                qf[ks][0] = gid < nq ? qp[gid * (D / 2) + at32] : 0u;
-                qf[ks][1] = gid < nq ? qp[gid * (D / 2) + at32 + 4] : 0u;
-                if (kWide) {
-                    qf[ks][2] = gid + 8 < nq ? qp[(gid + 8) * (D / 2) + at32] : 0u;
-                    qf[ks][3] = gid + 8 < nq ? qp[(gid + 8) * (D / 2) + at32 + 4] : 0u;
-                }
-            }
-            lp = a.logits + ((size_t)head * a.G + g0 + gid) * lp_row + 2 * tig;
+            run.reset();
+            run.read_q(a.q + ((size_t)head * a.G + g0) * D, nq);
+            lp = a.logits + ((size_t)head * a.G + g0 + gid) * lp_row;
         }
         if (valid > 0) {
-            // logits of 16 rows: two tiles of 8 rows, two chains each
-            float c[2][2][4] = {};
-            const uint32_t sk = k_at + stage * S::kStage, sv = v_at + stage * S::kStage;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                uint32_t b0, b1, b2, b3;
-                ldsm4(sk ^ (ks << 5), b0, b1, b2, b3);
-                const uint32_t a1 = kWide ? qf[ks][kWide ? 2 : 0] : 0u, a3 = kWide ? qf[ks][kWide ? 3 : 0] : 0u;
-                Pair<T>::mma(c[ks & 1][0], qf[ks][0], a1, qf[ks][1], a3, b0, b1);
-                Pair<T>::mma(c[ks & 1][1], qf[ks][0], a1, qf[ks][1], a3, b2, b3);
-            }
-            float t[2][2 * kR];               // [8-row tile][query head gid: 2 cached rows, gid + 8: 2]
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int i = 0; i < 2 * kR; ++i) t[n][i] = c[0][n][i] + c[1][n][i];
-            if (valid < kGroup) {
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2 * kR; ++i)
-                        if (n * 8 + 2 * tig + (i & 1) >= valid) t[n][i] = -INFINITY;
-            }
-            if (a.logits) {
-#pragma unroll
-                for (int r = 0; r < kR; ++r)
-                    if (gid + 8 * r < nq) {
-                        float* to = lp + m.row0 + r * 8 * lp_row;
-                        *(float2*)to = make_float2(t[0][2 * r], t[0][2 * r + 1]);
-                        *(float2*)(to + 8) = make_float2(t[1][2 * r], t[1][2 * r + 1]);
-                    }
-            }
-            uint32_t pa[4];                   // the weights as the A operand of P V
-#pragma unroll
-            for (int r = 0; r < kR; ++r) {
-                float mx = fmaxf(fmaxf(t[0][2 * r], t[0][2 * r + 1]), fmaxf(t[1][2 * r], t[1][2 * r + 1]));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * a.scale2;
-                if (__any_sync(0xffffffffu, mx > m_run[r])) {
-                    const float m_new = fmaxf(m_run[r], mx), f = ptx::ex2(m_run[r] - m_new);
-                    l_run[r] *= f;
-#pragma unroll
-                    for (int i = 0; i < kNt; ++i) {
-                        o[i][2 * r] *= f;
-                        o[i][2 * r + 1] *= f;
-                        if (!kWide) {         // rows 8-15 are the same query heads' remainders
-                            o[i][2] *= f;
-                            o[i][3] *= f;
-                        }
-                    }
-                    m_run[r] = m_new;
-                }
-                const float off = Pair<T>::kBias - m_run[r];
-                const float p0 = ptx::ex2(fmaf(t[0][2 * r], a.scale2, off)), p1 = ptx::ex2(fmaf(t[0][2 * r + 1], a.scale2, off));
-                const float p2 = ptx::ex2(fmaf(t[1][2 * r], a.scale2, off)), p3 = ptx::ex2(fmaf(t[1][2 * r + 1], a.scale2, off));
-                l_run[r] += (p0 + p1) + (p2 + p3);
-                pa[r] = Pair<T>::pack(p0, p1);
-                pa[r + 2] = Pair<T>::pack(p2, p3);
-                if (!kWide) {
-                    const float2 h0 = Pair<T>::unpack(pa[0]), h1 = Pair<T>::unpack(pa[2]);
-                    pa[1] = Pair<T>::pack(p0 - h0.x, p1 - h0.y);
-                    pa[3] = Pair<T>::pack(p2 - h1.x, p3 - h1.y);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kNt; i += 2) {
-                uint32_t b0, b1, b2, b3;
-                ldsm4t(sv ^ (i << 4), b0, b1, b2, b3);
-                Pair<T>::mma(o[i], pa[0], pa[1], pa[2], pa[3], b0, b1);
-                Pair<T>::mma(o[i + 1], pa[0], pa[1], pa[2], pa[3], b2, b3);
-            }
+            run.take(my_ring + stage * kStage, valid, a.scale2, [&](int r, int row, float x, float y) {
+                if (a.logits && gid + 8 * r < nq) *(float2*)(lp + r * 8 * lp_row + m.row0 + row) = make_float2(x, y);
+            });
         }
         if (m.valid_flags & kLast) {
             // ---- join the four warps' parts, each in the stage it has just consumed
             __syncwarp();
-            float* part = (float*)(ring + (size_t)(warp * kStages + stage) * S::kStage);
-#pragma unroll
-            for (int r = 0; r < (kWide ? 2 : 1); ++r) {
-                float l = l_run[r];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
-                const int row = gid + 8 * r;
-                if (tig == 0) sh_stat[warp][row] = make_float2(m_run[r], l);
-#pragma unroll
-                for (int i = 0; i < kNt; ++i) {
-                    const float x = kWide ? o[i][2 * r] : o[i][0] + o[i][2];
-                    const float y = kWide ? o[i][2 * r + 1] : o[i][1] + o[i][3];
-                    *(float2*)(part + row * D + ((i * 8 + 2 * tig) ^ ((row & 3) << 3))) = make_float2(x, y);
-                }
-            }
+            run.put_part((float*)(ring + (size_t)(warp * kStages + stage) * kStage), sh_stat[warp]);
             __syncthreads();
             const int slot = 2 * cta + (segment ? 1 : 0);
             const bool whole = m.valid_flags & kWhole;
             // a warp every kWarps-th query head, a lane kCols columns
             constexpr int kCols = D / 32;
             for (int row = warp; row < nq; row += kWarps) {
-                float2 st[kWarps];
-                float top = kLowest, l = 0.f, val[kCols] = {};
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) {
-                    st[x] = sh_stat[x][row];
-                    top = fmaxf(top, st[x].x);
-                }
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) {
-                    const float f = ptx::ex2(st[x].x - top);
-                    l += f * st[x].y;
-                    const float* from = (const float*)(ring + (size_t)(x * kStages + stage) * S::kStage) + row * D +
-                                        ((lane * kCols) ^ ((row & 3) << 3));
-#pragma unroll
-                    for (int c = 0; c < kCols; ++c) val[c] += f * from[c];
-                }
-                top -= Pair<T>::kBias;         // the sum and the output are 2^kBias larger
-                const size_t query = (size_t)head * a.G + g0 + row;
+                float val[kCols];
+                const int col = (lane * kCols) ^ run.part_swizzle(row);
+                const float2 st = add_parts<D, kWarps>(
+                    val, [&](int x) { return (const float*)(ring + (size_t)(x * kStages + stage) * kStage) + row * D + col; },
+                    [&](int x) { return sh_stat[x][row]; });
                 if (whole) {
-                    const float inv = l == 0.f ? 0.f : 1.f / l;     // a NaN sum stays one
-                    uint32_t packed[kCols / 2];
-#pragma unroll
-                    for (int c = 0; c < kCols; c += 2) packed[c / 2] = Pair<T>::pack(val[c] * inv, val[c + 1] * inv);
-#pragma unroll
-                    for (int c = 0; c < kCols / 2; ++c) ((uint32_t*)a.out)[(query * D + lane * kCols) / 2 + c] = packed[c];
-                    if (lane == 0) {
-                        const float lse2 = top + log2f(l);          // -inf where l is 0
-                        if (a.lse) a.lse[query] = lse2 * kLn2;
-                        if (a.lse2) a.lse2[query] = lse2;
-                        sh_lse2[row] = l == 0.f ? INFINITY : lse2;
-                    }
+                    const float lse2 = put_output<T, D>(a, (size_t)head * a.G + g0 + row, val, st);
+                    if (lane == 0) sh_lse2[row] = lse2;
                 } else {
                     float* to = a.parts + ((size_t)slot * a.gq + row) * D + lane * kCols;
 #pragma unroll
                     for (int c = 0; c < kCols; ++c) to[c] = val[c];
-                    if (lane == 0) a.stats[(size_t)slot * a.gq + row] = make_float2(top, l);
+                    if (lane == 0) a.stats[(size_t)slot * a.gq + row] = make_float2(st.x - Pair<T>::kBias, st.y);
                 }
             }
             __syncthreads();
