@@ -301,8 +301,8 @@ KVP_API kvp_status kvp_cache_append(const kvp_cache_shape* shape, const uint16_t
  *   workspace  at least kvp_cache_attend_workspace_bytes(shape, acc != NULL) bytes
  * Arithmetic: products of the inputs' type accumulated in fp32; logits, maximum, sums and joins
  * in fp32. The weights that multiply v are rounded to the inputs' type: as a pair (value and
- * remainder) when G <= 8. The cache is cut by its rows and the launch alone, and parts are joined
- * in a fixed order: repeat calls agree bit for bit.
+ * remainder) when G <= 8. The cache is cut by the shape and its rows alone, and parts are joined in
+ * a fixed order: repeat calls agree bit for bit.
  */
 KVP_API size_t kvp_cache_attend_workspace_bytes(const kvp_cache_shape* shape, int32_t accumulate);
 KVP_API kvp_status kvp_cache_attend(const kvp_cache_shape* shape, const uint16_t* q, const uint16_t* k_pages,

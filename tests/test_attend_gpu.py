@@ -8,6 +8,14 @@ from tests.cache_utils import Cache, attend_ref, bits, f64, kvp
 
 pytestmark = pytest.mark.gpu
 
+# Few heads whose tables hold at most 4096 rows are attended by a cluster of CTAs each; tables that
+# hold more, by runs of rows cut over all SMs. Both are put to the same cases.
+both = pytest.mark.parametrize("long_table", [False, True])
+
+
+def width_of(long_table, page):
+    return 4096 // page + 1 if long_table else None
+
 
 def attend(c, acc=True, table=None, lens=None, k=None, v=None, stream=None, workspace=None):
     m = kvp()
@@ -50,14 +58,15 @@ def check(c, got, present=None, lens=None):
 EDGES = [0, 1, 2, 15, 16, 17, 63, 64, 65, 127, 129, 300]
 
 
+@both
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("hq,hkv,d,page", [(4, 2, 64, 16), (8, 8, 128, 32), (7, 1, 128, 64), (16, 2, 64, 128),
                                            (24, 2, 128, 16), (16, 1, 128, 256), (17, 1, 64, 16), (64, 1, 128, 64),
                                            (66, 2, 64, 32)])
-def test_edges_of_length(dtype, hq, hkv, d, page):
+def test_edges_of_length(dtype, hq, hkv, d, page, long_table):
     b = -(-len(EDGES) // hkv)
     lens = (EDGES + [5] * hkv)[:b * hkv]
-    c = Cache(hq * d + page, b, hq, hkv, d, page, lens, dtype)
+    c = Cache(hq * d + page, b, hq, hkv, d, page, lens, dtype, width_of(long_table, page))
     check(c, attend(c))
     out, lse, _ = attend(c, acc=False)
     check(c, (out, lse, None))
@@ -71,30 +80,38 @@ def test_edges_of_length(dtype, hq, hkv, d, page):
     (40, 8, 8, 64, 16, list(range(0, 640, 2))),                   # many short heads
     (300, 4, 4, 64, 16, [0] * 1100 + [70] * 100),                 # long stretches of empty heads
     (1, 4, 2, 64, 16, [512, 512]),                                # the small layer
+    (2, 32, 8, 128, 16, [4096, 1, 4095, 0, 513, 4000, 512, 511] * 2),   # the most that a cluster takes
+    (1, 16, 1, 128, 16, [4090]),                                  # the same, 16 query heads
+    (1, 12, 1, 64, 256, [4096]),
+    (17, 1, 1, 64, 16, [i * 100 for i in range(17)]),             # one head too many for clusters
+    (1, 12, 1, 64, 256, [4097]),                                  # one row too many
 ])
 def test_real_lengths(b, hq, hkv, d, page, lens):
     c = Cache(b + d, b, hq, hkv, d, page, lens)
     check(c, attend(c))
 
 
-def test_all_heads_empty():
-    c = Cache(1, 3, 8, 2, 64, 16, [0] * 6)
+@both
+def test_all_heads_empty(long_table):
+    c = Cache(1, 3, 8, 2, 64, 16, [0] * 6, width=width_of(long_table, 16))
     out, lse, a = attend(c)
     assert (f64(out) == 0).all() and np.isneginf(f64(lse)).all()
     assert np.array_equal(bits(a), bits(c.acc))
 
 
-def test_lengths_outside_the_table_are_clamped():
-    c = Cache(2, 1, 4, 4, 64, 16, [48, 48, 20, 0])
-    wild = torch.tensor([[2 ** 30, 49, 20, -5]], dtype=torch.int32)
-    clamped = torch.tensor([[48, 48, 20, 0]], dtype=torch.int32)
+@pytest.mark.parametrize("most", [48, 4112])
+def test_lengths_outside_the_table_are_clamped(most):
+    c = Cache(2, 1, 4, 4, 64, 16, [most, most, 20, 0])
+    wild = torch.tensor([[2 ** 30, most + 1, 20, -5]], dtype=torch.int32)
+    clamped = torch.tensor([[most, most, 20, 0]], dtype=torch.int32)
     check(c, attend(c, lens=wild.cuda()), lens=clamped)
 
 
+@both
 @pytest.mark.parametrize("bad", [-1, -2 ** 31, "past", 2 ** 31 - 1])
-def test_entries_that_are_no_page(bad):
+def test_entries_that_are_no_page(bad, long_table):
     """Rows of an entry outside the pool draw no weight; a head with no page at all is an empty one."""
-    c = Cache(3, 2, 8, 2, 128, 16, [100, 64, 33, 200])
+    c = Cache(3, 2, 8, 2, 128, 16, [100, 64, 33, 200], width=width_of(long_table, 16))
     bad = c.num_pages if bad == "past" else bad
     table = c.table.clone().view(4, -1)
     table[0, 2], table[1, :], table[2, 2], table[3, 0], table[3, 12] = bad, bad, bad, bad, bad
@@ -105,8 +122,9 @@ def test_entries_that_are_no_page(bad):
     assert (f64(got[0])[0, 4:] == 0).all()
 
 
-def test_output_in_place_of_the_queries():
-    c = Cache(4, 4, 28, 4, 128, 16, [(37 * i) % 900 for i in range(16)])
+@both
+def test_output_in_place_of_the_queries(long_table):
+    c = Cache(4, 4, 28, 4, 128, 16, [(37 * i) % 900 for i in range(16)], width=width_of(long_table, 16))
     out, lse, _ = attend(c, acc=False)
     q = c.gpu("q")
     k, v, table, lens = c.gpu("k", "v", "table", "lens")
@@ -114,10 +132,12 @@ def test_output_in_place_of_the_queries():
     assert np.array_equal(bits(q), bits(out))
 
 
-def test_infinite_and_nan_rows_behave_as_in_a_softmax():
+@both
+def test_infinite_and_nan_rows_behave_as_in_a_softmax(long_table):
     """A key that makes a head's logit -inf has no weight; a NaN among a head's rows makes that head's
     output NaN and no other's."""
-    c = Cache(5, 1, 3, 3, 64, 16, [100, 100, 100], garbage=0.0, outliers=False)
+    width = width_of(long_table, 16)
+    c = Cache(5, 1, 3, 3, 64, 16, [100, 100, 100], garbage=0.0, outliers=False, width=width)
     c.q[:] = c.q.abs() + 0.5
     low = c.rows(0)[::3]
     c.k.view(-1, 64)[low] = float("-inf")
@@ -128,7 +148,7 @@ def test_infinite_and_nan_rows_behave_as_in_a_softmax():
     o = f64(out)
     assert np.isnan(o[0, 1]).all() and np.isnan(f64(lse)[0, 1])
     assert np.isnan(f64(a).reshape(-1)[c.rows(1).numpy()]).all()
-    ref = Cache(5, 1, 3, 3, 64, 16, [100, 100, 100], garbage=0.0, outliers=False)
+    ref = Cache(5, 1, 3, 3, 64, 16, [100, 100, 100], garbage=0.0, outliers=False, width=width)
     ref.q[:] = ref.q.abs() + 0.5
     r_out, _, r_w, t_out, _, t_w = attend_ref(ref, present=present)
     for h in (0, 2):
@@ -137,8 +157,9 @@ def test_infinite_and_nan_rows_behave_as_in_a_softmax():
     assert (drawn[::3] == 0).all()
 
 
-def test_every_logit_minus_infinity_is_an_empty_row():
-    c = Cache(6, 1, 2, 1, 64, 16, [40], garbage=0.0)
+@both
+def test_every_logit_minus_infinity_is_an_empty_row(long_table):
+    c = Cache(6, 1, 2, 1, 64, 16, [40], garbage=0.0, width=width_of(long_table, 16))
     c.q[:] = 1.0
     c.k.view(-1, 64)[c.rows(0)] = float("-inf")
     out, lse, a = attend(c)
@@ -146,19 +167,21 @@ def test_every_logit_minus_infinity_is_an_empty_row():
     assert np.array_equal(bits(a), bits(c.acc))
 
 
+@both
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
-def test_far_apart_logits(dtype):
+def test_far_apart_logits(dtype, long_table):
     """One row far above the others, near the start and near the end of the cache: the running
     maximum jumps, and the others' weights fall below what a float holds."""
     for at in (3, 700):
-        c = Cache(7, 1, 4, 1, 128, 32, [777], dtype, outliers=False)
+        c = Cache(7, 1, 4, 1, 128, 32, [777], dtype, outliers=False, width=width_of(long_table, 32))
         c.q[:] = c.q * 2
         c.k.view(-1, 128)[c.rows(0)[at]] = (c.q[0, 0].float() * 4).to(dtype)
         check(c, attend(c))
 
 
-def test_repeat_calls_agree_bit_for_bit():
-    c = Cache(8, 2, 32, 8, 128, 16, [(997 * i) % 6000 for i in range(16)])
+@both
+def test_repeat_calls_agree_bit_for_bit(long_table):
+    c = Cache(8, 2, 32, 8, 128, 16, [(997 * i) % (6000 if long_table else 4000) for i in range(16)])
     first = attend(c)
     for _ in range(3):
         again = attend(c)
@@ -167,8 +190,8 @@ def test_repeat_calls_agree_bit_for_bit():
 
 
 def test_split_does_not_depend_on_the_table_width():
-    """A table with room for far more rows gives the same bits (only lens says what there is)."""
-    c = Cache(9, 1, 8, 2, 128, 16, [1000, 333])
+    """A long table with room for yet more rows gives the same bits (only lens says what there is)."""
+    c = Cache(9, 1, 8, 2, 128, 16, [1000, 333], width=300)
     wide = Cache(9, 1, 8, 2, 128, 16, [1000, 333], width=4096, spare=0)
     wide.num_pages, wide.k, wide.v, wide.acc, wide.q = c.num_pages, c.k, c.v, c.acc, c.q
     table = torch.full((1, 2, 4096), -1, dtype=torch.int32)
@@ -178,8 +201,9 @@ def test_split_does_not_depend_on_the_table_width():
         assert np.array_equal(bits(x), bits(y))
 
 
-def test_two_streams_with_a_workspace_each():
-    cs = [Cache(10 + i, 1, 32, 8, 128, 16, [4000 + i] * 8) for i in range(2)]
+@both
+def test_two_streams_with_a_workspace_each(long_table):
+    cs = [Cache(10 + i, 1, 32, 8, 128, 16, [4000 + i] * 8, width=width_of(long_table, 16)) for i in range(2)]
     want = [attend(c) for c in cs]
     m = kvp()
     streams = [torch.cuda.Stream() for _ in cs]
@@ -201,10 +225,11 @@ def test_two_streams_with_a_workspace_each():
             assert np.array_equal(bits(x), bits(y))
 
 
-def test_captured_and_replayed_with_new_lengths():
+@pytest.mark.parametrize("width", [40, 200])
+def test_captured_and_replayed_with_new_lengths(width):
     """A graph reads lens and the table when it runs: lengths may change between replays."""
-    c = Cache(11, 2, 8, 4, 128, 32, [500, 3, 0, 64, 900, 17, 260, 1], width=40)
-    c2 = Cache(11, 2, 8, 4, 128, 32, [500, 3, 0, 64, 900, 17, 260, 1], width=40)
+    c = Cache(11, 2, 8, 4, 128, 32, [500, 3, 0, 64, 900, 17, 260, 1], width=width)
+    c2 = Cache(11, 2, 8, 4, 128, 32, [500, 3, 0, 64, 900, 17, 260, 1], width=width)
     m = kvp()
     q, k, v, table, lens, acc = c.gpu("q", "k", "v", "table", "lens", "acc")
     out, lse = torch.empty_like(q), torch.empty((c.b, c.hq), device="cuda")

@@ -16,9 +16,13 @@
 // (unnormalised output, maximum, sum) in the workspace.
 // attend_join: joins the parts of the units that were cut (a CTA has two at most), in the order of
 // the rows.
+// attend_short (few heads with short caches, as an eviction leaves them): a cluster of 8 CTAs a head,
+// one launch. All of a head's rows are in flight at once; the CTAs' parts are joined through
+// distributed shared memory and the logits never leave the SM.
 // The weights that acc gains need the final sum, so the logits go through the workspace (4 G bytes
 // a row against 4 d of the row itself) and are read back, mostly from L2, by the CTA that finished
 // the unit, or by attend_join for units that were cut.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -27,6 +31,8 @@
 
 #include "kvp_cache.cuh"
 #include "kvp_ptx.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace kvp {
 namespace {
@@ -42,6 +48,10 @@ constexpr int kLongRun = 32;                      // tiles of a run from which r
 constexpr int kShortRun = 6;                      // and tiles of the short runs that do it
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinPieces = 4;                    // blocks of attend_join that weigh one share, at most
+constexpr int kCluster = 8;                       // CTAs of attend_short for a head,
+constexpr int kShortWarps = 8, kShortThreads = kShortWarps * 32;
+constexpr int kShortRows = 512;                   // rows each may have,
+constexpr int kShortCtas = 128;                   // and CTAs in all: two clusters in each of eight GPCs
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.4028234663852886e38f;  // of a maximum over nothing: finite, so that
                                                     // differences of maxima are never inf - inf
@@ -713,6 +723,148 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
     }
 }
 
+// (kStages: as many groups of a warp as fit in flight beside the logits; a warp has 4 at most.)
+template <typename T, int D, bool kWide, int kStages>
+struct Short {
+    static constexpr int kQ = Running<T, D, kWide>::kQ;
+    static constexpr int kStage = Group16<D>::kStage;
+    static constexpr int kLogitRow = kShortRows + 8;            // floats of a query head's logits: eight
+                                                                // query heads' pairs in distinct banks
+    static constexpr size_t kRing = (size_t)kShortWarps * kStages * kStage;
+    static constexpr size_t kSmem = kRing + (size_t)kQ * kLogitRow * sizeof(float) + kRingAlign;
+    static_assert(kQ * D * 4 <= kStage, "a warp's part is joined in a stage");
+    static_assert(kShortRows / kGroup <= 4 * kShortWarps, "a warp has at most 4 groups");
+};
+
+template <typename T, int D, bool kWide, int kStages>
+__global__ void __launch_bounds__(kShortThreads, 1) attend_short(const AttendArgs a) {
+    using S = Short<T, D, kWide, kStages>;
+    constexpr int kStage = S::kStage, kQ = S::kQ, kCols = D / 32;
+    extern __shared__ __align__(16) uint8_t raw[];
+    uint8_t* const ring = raw + (-ptx::smem_u32(raw) & (kRingAlign - 1));
+    float* const logits = (float*)(ring + S::kRing);            // [kQ][kLogitRow]
+    __shared__ float2 warp_stat[kShortWarps][kQ], cta_stat[kQ];
+    __shared__ __align__(16) float cta_part[kQ][D];
+    __shared__ float sh_lse2[kQ];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2;
+    const int head = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, nq = a.G;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    Running<T, D, kWide> run;
+    run.reset();
+    run.read_q(a.q + (size_t)head * a.G * D, nq);
+    const int len = a.c.len(head);
+    if (len == 0) {                                             // the same in every CTA of the cluster
+        if (rank == 0) {
+            for (int e = tid; e < nq * D; e += kShortThreads) ((T*)a.out)[(size_t)head * nq * D + e] = T(0.f);
+            if (a.lse && tid < nq) a.lse[(size_t)head * nq + tid] = -INFINITY;
+        }
+        return;
+    }
+    // groups [first, last) of the head's are this CTA's; this warp's i-th is first + warp + kShortWarps i
+    const int groups = (len + kGroup - 1) / kGroup, per = (groups + kCluster - 1) / kCluster;
+    const int first = min(groups, rank * per), last = min(groups, first + per);
+    const int mine = max(0, (last - first - warp + kShortWarps - 1) / kShortWarps);
+    const int page_mask = (1 << a.c.page_shift) - 1;
+    int pages = -1;                                             // lane i: of this warp's i-th group
+    if (lane < mine) {
+        const int p = a.c.table[(size_t)head * a.c.max_pages + ((first + warp + kShortWarps * lane) * kGroup >> a.c.page_shift)];
+        if (p < a.c.num_pages) pages = p;
+    }
+    const Group16<D> group(a);
+    const uint32_t my_ring = ptx::smem_u32(ring) + warp * kStages * kStage;
+    auto valid_of = [&](int i) {
+        return __shfl_sync(0xffffffffu, pages, i) < 0 ? 0 : min(kGroup, len - (first + warp + kShortWarps * i) * kGroup);
+    };
+    auto fetch = [&](int i) {
+        if (i < mine) {
+            const int valid = valid_of(i), row0 = (first + warp + kShortWarps * i) * kGroup;
+            const int page = __shfl_sync(0xffffffffu, pages, i);
+            group.fetch(my_ring + i % kStages * kStage, ((size_t)max(page, 0) << a.c.page_shift) + (row0 & page_mask), valid);
+        }
+        cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) fetch(i);
+    // what this thread's four rows have drawn so far
+    const int row_first = first * kGroup, row_last = min(len, last * kGroup), j = row_first + tid * 4;
+    long long acc_row = -1;
+    float4 drawn = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.acc && j < row_last) {
+        acc_row = a.c.row(head, j);                             // four rows lie in one page
+        if (acc_row >= 0) drawn = *(const float4*)(a.acc + acc_row);
+    }
+    for (int i = 0; i < mine; ++i) {
+        cp_wait<kStages - 1>();
+        __syncwarp();
+        const int valid = valid_of(i);
+        if (valid > 0) {
+            float* to = logits + gid * S::kLogitRow + (warp + kShortWarps * i) * kGroup;
+            run.take(my_ring + i % kStages * kStage, valid, a.scale2, [&](int r, int row, float x, float y) {
+                if (a.acc) *(float2*)(to + r * 8 * S::kLogitRow + row) = make_float2(x, y);
+            });
+        }
+        __syncwarp();                                           // the stage has been read
+        fetch(i + kStages);
+    }
+    // ---- join the warps' parts, then the CTAs'
+    run.put_part((float*)(ring + (size_t)warp * kStages * kStage), warp_stat[warp]);
+    __syncthreads();
+    for (int row = warp; row < nq; row += kShortWarps) {
+        float val[kCols];
+        const int col = (lane * kCols) ^ run.part_swizzle(row);
+        const float2 st = add_parts<D, kShortWarps>(
+            val, [&](int x) { return (const float*)(ring + (size_t)x * kStages * kStage) + row * D + col; },
+            [&](int x) { return warp_stat[x][row]; });
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) cta_part[row][lane * kCols + c] = val[c];
+        if (lane == 0) cta_stat[row] = st;
+    }
+    ptx::cluster_arrive();
+    ptx::cluster_wait();
+    cg::cluster_group cluster = cg::this_cluster();
+    for (int row = warp; row < nq; row += kShortWarps) {
+        float val[kCols];
+        auto stat = [&](int x) { return *cluster.map_shared_rank(&cta_stat[row], x); };
+        if (row % kCluster == rank) {                           // its output is this CTA's to write
+            const float2 st = add_parts<D, kCluster>(
+                val, [&](int x) { return (const float*)cluster.map_shared_rank(&cta_part[row][lane * kCols], x); }, stat);
+            const float lse2 = put_output<T, D>(a, (size_t)head * nq + row, val, st);
+            if (lane == 0) sh_lse2[row] = lse2;
+        } else if (a.acc) {
+            float2 st = lane < kCluster ? stat(lane) : make_float2(kLowest, 0.f);
+            float top = st.x;
+#pragma unroll
+            for (int o = kCluster / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            float l = st.y * ptx::ex2(st.x - top);
+#pragma unroll
+            for (int o = kCluster / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (lane == 0) sh_lse2[row] = l == 0.f ? INFINITY : top - Pair<T>::kBias + log2f(l);
+        }
+    }
+    ptx::cluster_arrive();                                      // this thread has read the others' shared memory
+    __syncthreads();
+    if (acc_row >= 0 && KVP_CHECK(acc_row + 3 < ((long long)a.c.num_pages << a.c.page_shift), 602, head, j)) {
+        for (int g = 0; g < nq; ++g) {
+            const float4 t = *(const float4*)(logits + g * S::kLogitRow + tid * 4);
+            const float l = sh_lse2[g];
+            drawn.x += ptx::ex2(fmaf(t.x, a.scale2, -l));
+            drawn.y += ptx::ex2(fmaf(t.y, a.scale2, -l));
+            drawn.z += ptx::ex2(fmaf(t.z, a.scale2, -l));
+            drawn.w += ptx::ex2(fmaf(t.w, a.scale2, -l));
+        }
+        float* to = a.acc + acc_row;
+        if (j + 4 <= row_last) {
+            *(float4*)to = drawn;
+        } else {
+            to[0] = drawn.x;
+            if (j + 1 < row_last) to[1] = drawn.y;
+            if (j + 2 < row_last) to[2] = drawn.z;
+        }
+    }
+    ptx::cluster_wait();                                        // its shared memory outlives its readers
+}
+
 // A warp's sum over the parts of a unit for query head `row`: log2 of it, and (mine) the maximum
 // of part `lane`.
 __device__ __forceinline__ float joined_lse2(const AttendArgs& a, const Cut& p, int row, float& mine) {
@@ -876,9 +1028,39 @@ cudaError_t launch_split(const AttendArgs& a, int grid, cudaStream_t st) {
     return launch_dependent(kernel, grid, kThreads, smem, st, a);
 }
 
+template <typename T, int D, bool kWide, int kStages>
+cudaError_t launch_short(const AttendArgs& a, cudaStream_t st) {
+    auto kernel = attend_short<T, D, kWide, kStages>;
+    constexpr size_t smem = Short<T, D, kWide, kStages>::kSmem;
+    const cudaError_t e = allow_dynamic_smem((const void*)kernel, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.c.heads * kCluster));
+    cfg.blockDim = dim3(kShortThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 template <typename T, int D>
 cudaError_t launch_all(AttendArgs a, cudaStream_t st) {
     constexpr int kStages = D == 128 ? 3 : 6;
+    // One launch where heads are so few that their clusters run at once, and no table holds more rows
+    // than a cluster takes. (8 heads of 2111 rows: 6.6 us, 9.3 by
+    // attend_split and attend_join; 2 heads of 512: 3.9, 6.7.)
+    if (a.ng == 1 && a.c.heads * kCluster <= std::min(kShortCtas, num_sms()) && a.c.cap() <= kCluster * kShortRows) {
+        if (a.gq == 16) return launch_short<T, D, true, D == 128 ? 2 : 4>(a, st);
+        return launch_short<T, D, false, D == 128 ? 3 : 4>(a, st);
+    }
     // as many CTAs as are resident at once, but no more than there can be tiles, and as many with
     // short runs where runs can be long
     const long long most = (long long)a.c.heads * a.ng * ((a.c.cap() + kTile - 1) / kTile);

@@ -82,10 +82,6 @@ __device__ __forceinline__ void sync_all() {
     else __syncthreads();
 }
 
-// The cluster's barrier in two halves: all threads of the cluster arrive, all wait.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
 template <int C>
 __global__ void __launch_bounds__(kMaxThreads, 1) evict_select_long(const EvictArgs a) {
     extern __shared__ __align__(16) uint32_t keys[];
@@ -445,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
     const int t = a.budgets ? min(max(a.budgets[head], max(a.s + a.w, 1)), a.B) : a.B;
     const int w = a.w, s = a.s;
     const bool full = n > t;
-    if (C > 1) cluster_arrive();                     // this thread has read lens
+    if (C > 1) ptx::cluster_arrive();                     // this thread has read lens
     const int split = full ? t - w : n;              // rows below keep their places, or are replaced
     int32_t* src = a.src ? a.src + (size_t)head * a.B : nullptr;
     const bool fill = C == 1;                        // (a cluster leaves it to evict_move)
@@ -512,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
         }
     }
     if (!full) {
-        if (C > 1) cluster_wait();
+        if (C > 1) ptx::cluster_wait();
         if (rank == 0 && tid == 0) {
             a.info[head] = make_int4(n, t, 0, 0);
             a.lens_out[head] = n;
@@ -529,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
             if (!(cand >> i & 1)) key[i] = 0;
     }
     for (int i = tid; i < 4 * kBins; i += threads) (&sh.hist[0][0])[i] = 0;
-    if (C > 1) cluster_wait();                       // every CTA of the cluster runs and has read lens
+    if (C > 1) ptx::cluster_wait();                       // every CTA of the cluster runs and has read lens
     __syncthreads();
 
     // ---- T: the largest value that at least kk keys reach

@@ -240,6 +240,10 @@ __device__ __forceinline__ void launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A cluster's barrier in two halves: all threads of the cluster arrive, all wait.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Makes this thread's ordinary (generic-proxy) writes to shared memory visible to the
 // async proxy: operands the tensor cores read through descriptors.
 __device__ __forceinline__ void fence_proxy_async_smem() {
