@@ -250,7 +250,8 @@ KVP_API kvp_status kvp_score_static_status(void* stream);
  *                                       zero in the attention and for the eviction).
  *   lens  [b, hkv] int32                rows in use, taken as clamped to [0, M P]
  *   acc   [num_pages, P] fp32           the attention weight each cached row has drawn so far
- * No two live rows may share a place in the pool when a call writes to it. A cache with pages
+ * No two live rows may share a place in the pool when a call writes to it, and the tensors that a
+ * call reads may not overlap those it writes unless it says so. A cache with pages
  * of all heads ([pages, hkv, P, d]) is this one with pages numbered page * hkv + head; a
  * contiguous [b, hkv, B, d] (kvp_compact's output) is a pool of b hkv B / P pages when P
  * divides B. Rows at or past a head's len are left as they were.
@@ -298,7 +299,9 @@ KVP_API kvp_status kvp_cache_append(const kvp_cache_shape* shape, const uint16_t
  *   q    [b, hq, d];  out [b, hq, d] output, may be q itself
  *   lse  [b, hq] fp32 output, may be NULL
  *   acc  updated in place, may be NULL
- *   workspace  at least kvp_cache_attend_workspace_bytes(shape, acc != NULL) bytes
+ *   workspace  at least kvp_cache_attend_workspace_bytes(shape, acc != NULL) bytes (with acc 4 b hq
+ *           M P of them for logits: size the table to what the cache may hold); 0 for a bad shape,
+ *           or one of 2^31 or more tiles of 64 rows (b hkv ceil(G / 16) ceil(M P / 64))
  * Arithmetic: products of the inputs' type accumulated in fp32; logits, maximum, sums and joins
  * in fp32. The weights that multiply v are rounded to the inputs' type: as a pair (value and
  * remainder) when G <= 8. The cache is cut by the shape and its rows alone, and parts are joined in
@@ -331,7 +334,8 @@ typedef struct {
  *   lens_out [b, hkv] int32 output, may be lens itself: min(n, t)
  *   src      [b, hkv, B] int32 output, may be NULL: src[b, h, i] = the row that is now row i (-1
  *            at and past lens_out), to carry along what else a program keeps per row
- *   workspace  at least kvp_cache_evict_workspace_bytes(shape, evict) bytes
+ *   workspace  at least kvp_cache_evict_workspace_bytes(shape, evict) bytes (0 for a bad shape or
+ *           policy)
  * A row that moves from or to a place without a page is not copied. Pages past
  * ceil(lens_out / P) hold no rows any more and may be given to others.
  */

@@ -275,6 +275,47 @@ def test_decode_after_a_prefill_eviction(adaptive):
             assert torch.equal(cache.acc.cpu().view(-1)[rows[u][:len(src)]], weights.view(-1)[rows[u][src]])
 
 
+def test_refused_tensors():
+    """Types, shapes, strides and devices are checked before anything is launched."""
+    m = kvp()
+    c = Cache(1, 2, 4, 2, 64, 16, [20, 30, 0, 9])
+    sh = c.shape
+    q, k, v, table, lens, acc = c.gpu("q", "k", "v", "table", "lens", "acc")
+    out, lens2, kn = torch.empty_like(q), torch.empty_like(lens), torch.zeros((2, 2, 1, 64), dtype=q.dtype, device="cuda")
+    ws = m.attend_workspace_for(sh, True)
+    attend = dict(q=q, k_pages=k, v_pages=v, table=table, lens=lens, out=out, lse=None, acc=acc, workspace=ws)
+    append = dict(k_new=kn, v_new=kn, k_pages=k, v_pages=v, table=table, lens=lens, lens_out=lens2, acc=acc)
+    evict = dict(evict=m.make_evict(8, 1, 2), k_pages=k, v_pages=v, acc=acc, acc_out=acc, table=table, lens=lens,
+                 lens_out=lens2)
+    before = [t.clone() for t in (q, k, v, lens, acc)]
+    for call, good in ((m.kvp_cache_attend, attend), (m.kvp_cache_append, append), (m.kvp_cache_evict, evict)):
+        for name, t in good.items():
+            if not isinstance(t, torch.Tensor) or name == "workspace":
+                continue
+            wrong = [t.cpu(), t.to(torch.float64), t[:0] if t.dim() else t, None, 3]
+            wrong.append(torch.empty(t.shape + (2,), dtype=t.dtype, device="cuda")[..., 0])        # strided
+            if name == "acc" and call is not m.kvp_cache_evict:
+                wrong.remove(None)
+            for bad in wrong:
+                with pytest.raises(ValueError):
+                    call(sh, **{**good, name: bad})
+        with pytest.raises(ValueError):
+            call(m.make_shape(1, 8, 2, 64, 128, 16, 32), **good)                     # another call's shape
+    with pytest.raises(ValueError):
+        m.kvp_cache_evict(sh, **{**evict, "evict": m.make_policy()})
+    with pytest.raises(m.KvpError) as e:
+        m.kvp_cache_attend(sh, **{**attend, "workspace": ws[:ws.numel() - 256]})
+    assert e.value.status == 4
+    with pytest.raises(m.KvpError) as e:
+        m.kvp_cache_evict(sh, **{**evict, "evict": m.make_evict(8, 6, 3)}, workspace=ws)
+    assert e.value.status == 2
+    with pytest.raises(ValueError):
+        m.LayerCache(1, 4, 2, 64, 64, 16, m.make_evict(64, 1, 2))
+    torch.cuda.synchronize()
+    for t, b in zip((q, k, v, lens, acc), before):
+        assert np.array_equal(bits(t), bits(b))
+
+
 def test_a_captured_step_replays():
     """A whole step (append, attend, evict) in a graph: lens advances on the device from replay to
     replay, and the results are those of steps called one by one."""

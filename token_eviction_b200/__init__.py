@@ -415,12 +415,20 @@ def _cache_workspace(nbytes, what, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
 
 
+def _structure(x, kind):
+    if not isinstance(x, kind):
+        raise ValueError(f"{type(x).__name__} where a {kind.__name__} is wanted")
+    return x
+
+
 def attend_workspace_for(shape, accumulate=False, device=None) -> torch.Tensor:
+    _structure(shape, KvpCacheShape)
     n = int(_lib.kvp_cache_attend_workspace_bytes(ctypes.byref(shape), int(bool(accumulate))))
     return _cache_workspace(n, "kvp_cache_attend_workspace_bytes", device)
 
 
 def evict_workspace_for(shape, evict, device=None) -> torch.Tensor:
+    _structure(shape, KvpCacheShape), _structure(evict, KvpEvict)
     n = int(_lib.kvp_cache_evict_workspace_bytes(ctypes.byref(shape), ctypes.byref(evict)))
     return _cache_workspace(n, "kvp_cache_evict_workspace_bytes", device)
 
@@ -454,7 +462,7 @@ def kvp_cache_evict(shape, evict, k_pages, v_pages, acc, acc_out, table, lens, l
     """Each head keeps its first `sinks` rows, its last `window` and the heaviest between them, up to
     its budget (a KvpEvict, or a dict of make_evict's arguments). In place; acc_out may be acc
     and lens_out lens."""
-    ev = make_evict(**evict) if isinstance(evict, dict) else evict
+    ev = make_evict(**evict) if isinstance(evict, dict) else _structure(evict, KvpEvict)
     own = workspace is None
     if own:
         workspace = evict_workspace_for(shape, ev, _device_of(k_pages))
@@ -471,13 +479,15 @@ class LayerCache:
     a time appended, attended over and, where a budget is given, evicted by accumulated weight.
 
     Holds up to `capacity` rows per KV head, in pages of its own (table and pools may be replaced by
-    a program that shares a pool between layers or requests). `evict`: a KvpEvict; heads over its
-    budget are cut back in every step.
+    a program that shares a pool between layers or requests); rows past them are dropped. `evict`: a
+    KvpEvict; heads over its budget are cut back in every step, so capacity must exceed the budget.
     """
 
     def __init__(self, batch, hq, hkv, head_dim, capacity, page_size=64, evict: KvpEvict | None = None,
                  dtype=torch.bfloat16, device="cuda"):
         width = -(-capacity // page_size)
+        if evict is not None and width * page_size <= evict.budget:
+            raise ValueError("capacity must exceed the eviction's budget: a step appends before it evicts")
         self.shape = make_cache_shape(batch, hq, hkv, head_dim, page_size, batch * hkv * width, width, dtype)
         self.evict_policy = evict
         new = lambda shape, dt: torch.zeros(shape, dtype=dt, device=device)
