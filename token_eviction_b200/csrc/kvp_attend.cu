@@ -47,7 +47,7 @@ constexpr int kMaxGrid = 2 * kResident;           // the workspace holds parts f
 constexpr int kLongRun = 32;                      // tiles of a run from which runs of unequal speed are balanced
 constexpr int kShortRun = 6;                      // and tiles of the short runs that do it
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinPieces = 4;                    // blocks of attend_join that weigh one share, at most
+constexpr int kJoinPieces = 2;                    // blocks of attend_join that weigh one share, at most
 constexpr int kCluster = 8;                       // CTAs of attend_short for a head,
 constexpr int kShortWarps = 8, kShortThreads = kShortWarps * 32;
 constexpr int kShortRows = 512;                   // rows each may have,
