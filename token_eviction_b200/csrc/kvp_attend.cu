@@ -51,7 +51,7 @@ constexpr int kJoinPieces = 2;                    // blocks of attend_join that 
 constexpr int kCluster = 8;                       // CTAs of attend_short for a head,
 constexpr int kShortWarps = 8, kShortThreads = kShortWarps * 32;
 constexpr int kShortRows = 512;                   // rows each may have,
-constexpr int kShortCtas = 128;                   // and CTAs in all: two clusters in each of eight GPCs
+constexpr int kShortCtas = 120;                   // and CTAs in all: 15 clusters of 8 SMs find room on 148
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.4028234663852886e38f;  // of a maximum over nothing: finite, so that
                                                     // differences of maxima are never inf - inf
@@ -291,12 +291,13 @@ struct Walk {
         const int h = base + (threadIdx.x & 31);
         lane_len = h < c.heads ? c.len(h) : 0;
     }
-    __device__ __forceinline__ void begin(const CacheView& c, int ng, const Start& s) {
+    // `loaded`: lane_len holds the first 32 heads' lengths
+    __device__ __forceinline__ void begin(const CacheView& c, int ng, const Start& s, bool loaded) {
         head = s.unit / ng;
         sub = s.unit - head * ng;
         tile = s.tile;
         base = head & ~31;
-        load(c);
+        if (!loaded) load(c);
         len = __shfl_sync(0xffffffffu, lane_len, head & 31);
         nt = tiles_of(len);
     }
@@ -323,6 +324,28 @@ struct Walk {
         nt = tiles_of(len);
     }
 };
+
+// Of up to 32 heads every warp finds its CTA's run by itself, a length a lane, with no barrier and no
+// second read of the lengths.
+__device__ __forceinline__ Cutting find_start_32(const CacheView& c, int ng, int resident, Start* at, int* lane_len) {
+    const int lane = threadIdx.x & 31;
+    *lane_len = lane < c.heads ? c.len(lane) : 0;
+    const int nt = tiles_of(*lane_len), n = nt * ng;          // (at most 2^19 tiles each)
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    const Cutting cutting(__shfl_sync(0xffffffffu, inc, 31), resident, gridDim.x);
+    const int want = (int)cutting.begin(min((int)blockIdx.x, cutting.ctas()));
+    const unsigned past = __ballot_sync(0xffffffffu, inc > want);
+    const int head = past ? __ffs(past) - 1 : 0;
+    const int i = want - __shfl_sync(0xffffffffu, inc - n, head), head_tiles = max(1, __shfl_sync(0xffffffffu, nt, head));
+    at->unit = head * ng + i / head_tiles;
+    at->tile = i % head_tiles;
+    return cutting;
+}
 
 // What a warp notes about a group when it issues its loads and reads when it consumes it.
 struct __align__(16) Meta {
@@ -573,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
     extern __shared__ __align__(16) uint8_t raw[];
     uint8_t* const ring = raw + (-ptx::smem_u32(raw) & (kRingAlign - 1));
     __shared__ long long warp_sums[kWarps];
-    __shared__ Start at;
+    __shared__ Start sh_at;
     __shared__ Meta meta[kWarps][kStages];
     __shared__ float2 sh_stat[kWarps][kQ];
     __shared__ float sh_lse2[kQ];
@@ -582,7 +605,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
     const int grid = gridDim.x, cta = blockIdx.x;
 
     ptx::grid_dependency_wait();
-    const Cutting cutting = find_start(a.c, a.ng, a.resident, warp_sums, &at);
+    Start at;
+    Walk w;
+    const bool few = a.c.heads <= 32;
+    const Cutting cutting = few ? find_start_32(a.c, a.ng, a.resident, &at, &w.lane_len)
+                                : find_start(a.c, a.ng, a.resident, warp_sums, &sh_at);
+    if (!few) at = sh_at;
     ptx::launch_dependents();
     // heads without rows
     for (int h = cta; h < a.c.heads; h += grid) {
@@ -596,8 +624,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
     const int steps = (int)(cutting.begin(cta + 1) - r0);
 
     // ---- the issuing side: the walk is one tile ahead of its loads, so that its page is at hand
-    Walk w;
-    w.begin(a.c, a.ng, at);
+    w.begin(a.c, a.ng, at, few);
     const uint32_t my_ring = ptx::smem_u32(ring) + warp * kStages * kStage;
     // pages of the walk's unit, a lane each: of this warp's groups in tiles [page_base, page_base + 32)
     int page_base = 0, pages = -1;
@@ -649,6 +676,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
 
     // ---- the consuming side
     Running<T, D, kWide> run;
+    {                                         // the first unit's query heads, while its rows are on their way
+        const int first_head = at.unit / a.ng, first_g = (at.unit - first_head * a.ng) * a.gq;
+        run.read_q(a.q + ((size_t)first_head * a.G + first_g) * D, min(a.gq, a.G - first_g));
+    }
     int segment = 0, seg_step = 0;            // units begun before this one; the step that began it
     int head = 0, g0 = 0, nq = 0;             // the unit's head, first query head and how many
     float* lp = nullptr;                      // logits of query head gid of the unit
@@ -667,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
             g0 = m.sub * a.gq;
             nq = min(a.gq, a.G - g0);
             run.reset();
-            run.read_q(a.q + ((size_t)head * a.G + g0) * D, nq);
+            if (step > 0) run.read_q(a.q + ((size_t)head * a.G + g0) * D, nq);
             lp = a.logits + ((size_t)head * a.G + g0 + gid) * lp_row;
         }
         if (valid > 0) {
