@@ -11,7 +11,10 @@
 // memory; a cluster's CTAs write theirs into one another's shared memory. Every warp finds the
 // digit by itself, so that a round has one barrier (and one of the cluster). It ends as soon as
 // all keys that share T's bits stay. One scan of packed counts then gives every thread its places
-// in the lists. A head with few rows to copy is finished here.
+// in the lists. A head with few rows to copy is finished here; one that gives up few rows (a decode's
+// step: one) has them picked one by one instead, by every warp the lightest of its own rows and then by one
+// warp of all of those. (512 heads that give up one row of 2049: 7.2 us, 11.5 by rounds; rounds are
+// as fast from about 10 rows on.)
 // (Two bits a round by counting keys against three candidates, with no atomics: 28 us where this
 // takes 17 for 512 heads of 2064 rows.)
 // evict_select_long: longer rows, keys in shared memory or read again each round, four bits a round by
@@ -38,6 +41,7 @@ constexpr int kManyThreads = 384;         // most threads of the CTAs that share
 constexpr int kPerMost = 16;             // keys a thread of evict_select holds
 constexpr int kMoveThreads = 256, kMoveCtas = 3;   // of evict_move: threads, CTAs an SM
 constexpr int kMoveLoads = 8;            // 16-byte loads a lane of evict_move has in flight
+constexpr int kLight = 8;                // rows given up up to which evict_select picks them one by one, and
 constexpr int kFew = 64;                 // rows past t - w up to which evict_select copies them itself (one CTA a head)
 
 struct EvictArgs {
@@ -399,13 +403,17 @@ constexpr int kBins = 256;
 
 template <int C>
 struct PickShared {
-    __align__(16) uint32_t hist[4][kBins];           // of this CTA's keys, a digit a round
+    union {
+        __align__(16) uint32_t hist[4][kBins];       // of this CTA's keys, a digit a round; or
+        uint2 light[C == 1 ? kMaxWarps : 1][kLight]; // a warp's lightest rows, in the order they go: key, row
+    };
     __align__(16) uint32_t all[2][C > 1 ? C : 1][kBins];   // every CTA's, of the cluster
     unsigned long long warp_scan[kMaxWarps];         // packed counts: a warp's, then those before it
     unsigned long long cta_scan[C];                  // every CTA's
     uint32_t T;                                      // what warp 0 found in the last round
     int above;
     bool exact;
+    int listed;
     int from[kFew], to[kFew];                        // listed rows, where they are copied here;
     long long to_row[kFew];                          // where the places lie in the pool;
     long long row[kFew];                             // rows [t - w, n): where they lie (-1: no page),
@@ -524,149 +532,210 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
         for (int i = 0; i < kPer; ++i)
             if (!(cand >> i & 1)) key[i] = 0;
     }
-    for (int i = tid; i < 4 * kBins; i += threads) (&sh.hist[0][0])[i] = 0;
-    if (C > 1) ptx::cluster_wait();                       // every CTA of the cluster runs and has read lens
-    __syncthreads();
-
-    // ---- T: the largest value that at least kk keys reach
-    const int kk = t - s - w;                        // candidates that stay; there are more than kk
-    uint32_t T = kk > 0 ? 0u : 0xFFFFFFFFu;
-    int above = 0;                                   // keys known to lie above those that T's bits leave open
-    bool exact = kk == 0;                            // just kk keys reach T
-#pragma unroll
-    for (int round = 0; round < 4; ++round) {
-        if (exact) break;
-        const int bits = round < 3 ? 8 : 7, shift = round < 3 ? 23 - 8 * round : 0;
-        uint32_t* hist = sh.hist[round];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            // the bits above this digit are T's, and it is a candidate
-            if (key[i] != 0 && (round == 0 || (key[i] ^ T) >> (shift + bits) == 0))
-                atomicAdd(&hist[key[i] >> shift & ((1u << bits) - 1)], 1u);
-        }
-        __syncthreads();
-        if (C > 1) {                                 // every CTA gets every CTA's counts
-            for (int i = tid; i < C * kBins / 4; i += threads) {
-                uint4* to = (uint4*)sh.all[round & 1][rank] + i % (kBins / 4);
-                *cg::this_cluster().map_shared_rank(to, i / (kBins / 4)) = ((const uint4*)hist)[i % (kBins / 4)];
-            }
-            sync_all<C>();
-        }
-        if (warp == 0) {
-            // lane x: digits 255 - 8 x down to 248 - 8 x
-            int bin[8] = {};
-#pragma unroll
-            for (int x = 0; x < C; ++x) {
-                const uint4* from = (const uint4*)((C > 1 ? sh.all[round & 1][x] : hist) + kBins - 8 - 8 * lane);
-                const uint4 lo = from[0], hi = from[1];
-                bin[0] += hi.w, bin[1] += hi.z, bin[2] += hi.y, bin[3] += hi.x;
-                bin[4] += lo.w, bin[5] += lo.z, bin[6] += lo.y, bin[7] += lo.x;
-            }
-            int inc = ((bin[0] + bin[1]) + (bin[2] + bin[3])) + ((bin[4] + bin[5]) + (bin[6] + bin[7]));
-            const int sum = inc;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            const int want = kk - above;             // the want-th key from the top is T
-            if (inc - sum < want && want <= inc) {   // one lane: there are more than kk keys
-                int before = inc - sum, digit = 255 - 8 * lane, count = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    count = bin[i];
-                    if (before + count >= want) break;
-                    before += count;
-                    --digit;
-                }
-                sh.T = T | (uint32_t)digit << shift;
-                sh.above = above + before;
-                sh.exact = before + count == want;
-            }
-        }
-        __syncthreads();
-        T = sh.T;
-        above = sh.above;
-        exact = sh.exact;
-        // (warp 0 writes them again only after the next round's barrier)
-    }
-    // rows whose key is T that stay, lowest first; none is needed where just kk keys reach T
-    const int need_eq = exact ? 0 : kk - above;
-    uint32_t gt = 0, eqm = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        gt |= (exact ? key[i] >= T : key[i] > T) ? 1u << i : 0u;
-        eqm |= key[i] == T ? 1u << i : 0u;
-    }
-    if (exact) eqm = 0;
-
-    // ---- places in the lists: counts before this thread's rows
-    const unsigned long long mine = pack4(__popc(gt & low), __popc(eqm & low), __popc(gt & ~low), __popc(eqm & ~low));
-    unsigned long long before = warp_inclusive(mine) - mine;
-    if (lane == 31) sh.warp_scan[warp] = before + mine;
-    __syncthreads();
-    if (warp == 0) {
-        const unsigned long long v = lane < warps ? sh.warp_scan[lane] : 0ull, inc = warp_inclusive(v);
-        if (lane < warps) sh.warp_scan[lane] = inc - v;
-        const unsigned long long all = __shfl_sync(0xffffffffu, inc, 31);
-        if (C > 1) {
-            if (lane < C) *cg::this_cluster().map_shared_rank(&sh.cta_scan[rank], lane) = all;
-        } else if (lane == 0) {
-            sh.cta_scan[0] = all;
-        }
-    }
-    sync_all<C>();
-    before += sh.warp_scan[warp];
-    // 16 bits hold a CTA's counts, not a cluster's
-    int b_gt_low = (int)(before & 0xFFFF), b_eq_low = (int)(before >> 16 & 0xFFFF), b_gt_high = (int)(before >> 32 & 0xFFFF),
-        b_eq_high = (int)(before >> 48), all_eq_low = 0, all_gt_high = 0, all_eq_high = 0;
-#pragma unroll
-    for (int x = 0; x < C; ++x) {
-        const unsigned long long v = sh.cta_scan[x];
-        const int gl = (int)(v & 0xFFFF), el = (int)(v >> 16 & 0xFFFF), gh = (int)(v >> 32 & 0xFFFF), eh = (int)(v >> 48);
-        if (x < rank) b_gt_low += gl, b_eq_low += el, b_gt_high += gh, b_eq_high += eh;
-        all_eq_low += el;
-        all_gt_high += gh;
-        all_eq_high += eh;
-    }
-    // equal rows stay from the lowest on, and the low ones come first
-    const int listed = all_gt_high + min(all_eq_low + all_eq_high, need_eq) - min(all_eq_low, need_eq);
-    const int eq = b_eq_low + b_eq_high, room = max(0, need_eq - eq);    // equal rows before; of this thread's, that stay
-    const int kept_low = b_gt_low + min(b_eq_low, need_eq);
-    const int kept_high = b_gt_high + min(eq, need_eq) - min(b_eq_low, need_eq);
-    while (__popc(eqm) > room) eqm &= ~(1u << (31 - __clz(eqm)));         // drops the highest
-    const uint32_t kept = gt | eqm;
     int32_t* from = a.from + (size_t)head * a.B;
     int32_t* to = a.to + (size_t)head * a.B;
-    // evicted places: candidates before this thread's rows less those kept
-    int at = max(0, min(j0, n - w) - s) - kept_low;
-    for (uint32_t m = cand & low & ~kept; m; m &= m - 1, ++at) {
-        const int j = j0 + __ffs(m) - 1;
-        if (here) {
-            sh.to[at] = j;
-            sh.to_row[at] = a.c.row(head, j);
-        } else if (KVP_CHECK(at >= 0 && at < a.B, 701, head, at)) {
-            to[at] = j;
+    int listed = 0;
+    if (here && n - t <= kLight) {
+        // ---- the n - t rows that go, one by one: the smallest key, of equal ones the highest row
+        const int gone = n - t;
+        uint32_t least = 0xFFFFFFFFu;                // this thread's smallest key, and its highest row that has it
+        int which = 0;
+        auto look = [&]() {
+            least = 0xFFFFFFFFu;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (key[i] != 0 && key[i] <= least) least = key[i], which = i;
+        };
+        look();
+        for (int i = 0; i < gone; ++i) {
+            const uint32_t m = __reduce_min_sync(0xffffffffu, least);
+            const int owner = 31 - __clz(__ballot_sync(0xffffffffu, least == m));
+            if (lane == owner) {
+                sh.light[warp][i] = make_uint2(m, (uint32_t)(j0 + which));
+#pragma unroll
+                for (int x = 0; x < kPer; ++x)
+                    if (x == which) key[x] = 0;
+                look();
+            }
         }
-    }
-    at = kept_high;
-    for (uint32_t m = kept & ~low; m; m &= m - 1, ++at) {
-        const int j = j0 + __ffs(m) - 1;
-        if (here) sh.from[at] = j;
-        else if (KVP_CHECK(at < a.B, 702, head, at)) from[at] = j;
-    }
-    if (!fill) {
-        // evict_move fills in src and acc_out of the rows that stay: a bit each
-        const uint32_t stays = low & (kept | first_bits(s));
-        if (j0 < split) {
-            if (kPer == 16) ((uint16_t*)a.stays)[((size_t)head * a.stays_stride + j0 / 8) / 2] = (uint16_t)stays;
-            else a.stays[(size_t)head * a.stays_stride + j0 / 8] = (uint8_t)stays;
+        __syncthreads();
+        if (warp == 0) {
+            int taken = 0;                           // lane x: of warp x's rows
+            uint2 next = lane < warps ? sh.light[lane][0] : make_uint2(0xFFFFFFFFu, 0u);
+            uint32_t mine = 0xFFFFFFFFu;             // lane i: the i-th row that goes
+            for (int i = 0; i < gone; ++i) {
+                const uint32_t m = __reduce_min_sync(0xffffffffu, next.x);
+                const int owner = 31 - __clz(__ballot_sync(0xffffffffu, next.x == m));   // a higher warp has higher rows
+                const uint32_t row = __shfl_sync(0xffffffffu, next.y, owner);
+                if (lane == i) mine = row;
+                if (lane == owner) next = ++taken < gone ? sh.light[lane][taken] : make_uint2(0xFFFFFFFFu, 0u);
+            }
+            // [split, split + gone) are the candidates past split: those that stay take the places below it
+            const bool is_low = lane < gone && (int)mine < split;
+            const unsigned lows = __ballot_sync(0xffffffffu, is_low);
+            const uint32_t high_bit = lane < gone && !is_low ? 1u << (mine - split) : 0u;
+            const uint32_t stay_high = ((1u << gone) - 1) & ~__reduce_or_sync(0xffffffffu, high_bit);
+            int place = 0;                           // evicted places below this one
+            for (int x = 0; x < gone; ++x) {
+                const uint32_t other = __shfl_sync(0xffffffffu, mine, x);
+                place += (lows >> x & 1) && other < mine;
+            }
+            if (is_low) {
+                sh.to[place] = (int)mine;
+                sh.to_row[place] = a.c.row(head, (int)mine);
+            }
+            if (stay_high >> lane & 1) sh.from[__popc(stay_high & ((1u << lane) - 1))] = split + lane;
+            if (lane == 0) {
+                sh.listed = __popc(lows);
+                a.info[head] = make_int4(n, t, __popc(lows), 0);
+                a.lens_out[head] = t;
+            }
         }
+        __syncthreads();
+        listed = sh.listed;
+    } else {
+        for (int i = tid; i < 4 * kBins; i += threads) (&sh.hist[0][0])[i] = 0;
+        if (C > 1) ptx::cluster_wait();                       // every CTA of the cluster runs and has read lens
+        __syncthreads();
+
+        // ---- T: the largest value that at least kk keys reach
+        const int kk = t - s - w;                        // candidates that stay; there are more than kk
+        uint32_t T = kk > 0 ? 0u : 0xFFFFFFFFu;
+        int above = 0;                                   // keys known to lie above those that T's bits leave open
+        bool exact = kk == 0;                            // just kk keys reach T
+#pragma unroll
+        for (int round = 0; round < 4; ++round) {
+            if (exact) break;
+            const int bits = round < 3 ? 8 : 7, shift = round < 3 ? 23 - 8 * round : 0;
+            uint32_t* hist = sh.hist[round];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                // the bits above this digit are T's, and it is a candidate
+                if (key[i] != 0 && (round == 0 || (key[i] ^ T) >> (shift + bits) == 0))
+                    atomicAdd(&hist[key[i] >> shift & ((1u << bits) - 1)], 1u);
+            }
+            __syncthreads();
+            if (C > 1) {                                 // every CTA gets every CTA's counts
+                for (int i = tid; i < C * kBins / 4; i += threads) {
+                    uint4* to = (uint4*)sh.all[round & 1][rank] + i % (kBins / 4);
+                    *cg::this_cluster().map_shared_rank(to, i / (kBins / 4)) = ((const uint4*)hist)[i % (kBins / 4)];
+                }
+                sync_all<C>();
+            }
+            if (warp == 0) {
+                // lane x: digits 255 - 8 x down to 248 - 8 x
+                int bin[8] = {};
+#pragma unroll
+                for (int x = 0; x < C; ++x) {
+                    const uint4* from = (const uint4*)((C > 1 ? sh.all[round & 1][x] : hist) + kBins - 8 - 8 * lane);
+                    const uint4 lo = from[0], hi = from[1];
+                    bin[0] += hi.w, bin[1] += hi.z, bin[2] += hi.y, bin[3] += hi.x;
+                    bin[4] += lo.w, bin[5] += lo.z, bin[6] += lo.y, bin[7] += lo.x;
+                }
+                int inc = ((bin[0] + bin[1]) + (bin[2] + bin[3])) + ((bin[4] + bin[5]) + (bin[6] + bin[7]));
+                const int sum = inc;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += y;
+                }
+                const int want = kk - above;             // the want-th key from the top is T
+                if (inc - sum < want && want <= inc) {   // one lane: there are more than kk keys
+                    int before = inc - sum, digit = 255 - 8 * lane, count = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        count = bin[i];
+                        if (before + count >= want) break;
+                        before += count;
+                        --digit;
+                    }
+                    sh.T = T | (uint32_t)digit << shift;
+                    sh.above = above + before;
+                    sh.exact = before + count == want;
+                }
+            }
+            __syncthreads();
+            T = sh.T;
+            above = sh.above;
+            exact = sh.exact;
+            // (warp 0 writes them again only after the next round's barrier)
+        }
+        // rows whose key is T that stay, lowest first; none is needed where just kk keys reach T
+        const int need_eq = exact ? 0 : kk - above;
+        uint32_t gt = 0, eqm = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            gt |= (exact ? key[i] >= T : key[i] > T) ? 1u << i : 0u;
+            eqm |= key[i] == T ? 1u << i : 0u;
+        }
+        if (exact) eqm = 0;
+
+        // ---- places in the lists: counts before this thread's rows
+        const unsigned long long mine = pack4(__popc(gt & low), __popc(eqm & low), __popc(gt & ~low), __popc(eqm & ~low));
+        unsigned long long before = warp_inclusive(mine) - mine;
+        if (lane == 31) sh.warp_scan[warp] = before + mine;
+        __syncthreads();
+        if (warp == 0) {
+            const unsigned long long v = lane < warps ? sh.warp_scan[lane] : 0ull, inc = warp_inclusive(v);
+            if (lane < warps) sh.warp_scan[lane] = inc - v;
+            const unsigned long long all = __shfl_sync(0xffffffffu, inc, 31);
+            if (C > 1) {
+                if (lane < C) *cg::this_cluster().map_shared_rank(&sh.cta_scan[rank], lane) = all;
+            } else if (lane == 0) {
+                sh.cta_scan[0] = all;
+            }
+        }
+        sync_all<C>();
+        before += sh.warp_scan[warp];
+        // 16 bits hold a CTA's counts, not a cluster's
+        int b_gt_low = (int)(before & 0xFFFF), b_eq_low = (int)(before >> 16 & 0xFFFF), b_gt_high = (int)(before >> 32 & 0xFFFF),
+            b_eq_high = (int)(before >> 48), all_eq_low = 0, all_gt_high = 0, all_eq_high = 0;
+#pragma unroll
+        for (int x = 0; x < C; ++x) {
+            const unsigned long long v = sh.cta_scan[x];
+            const int gl = (int)(v & 0xFFFF), el = (int)(v >> 16 & 0xFFFF), gh = (int)(v >> 32 & 0xFFFF), eh = (int)(v >> 48);
+            if (x < rank) b_gt_low += gl, b_eq_low += el, b_gt_high += gh, b_eq_high += eh;
+            all_eq_low += el;
+            all_gt_high += gh;
+            all_eq_high += eh;
+        }
+        // equal rows stay from the lowest on, and the low ones come first
+        listed = all_gt_high + min(all_eq_low + all_eq_high, need_eq) - min(all_eq_low, need_eq);
+        const int eq = b_eq_low + b_eq_high, room = max(0, need_eq - eq);    // equal rows before; of this thread's, that stay
+        const int kept_low = b_gt_low + min(b_eq_low, need_eq);
+        const int kept_high = b_gt_high + min(eq, need_eq) - min(b_eq_low, need_eq);
+        while (__popc(eqm) > room) eqm &= ~(1u << (31 - __clz(eqm)));         // drops the highest
+        const uint32_t kept = gt | eqm;
+        // evicted places: candidates before this thread's rows less those kept
+        int at = max(0, min(j0, n - w) - s) - kept_low;
+        for (uint32_t m = cand & low & ~kept; m; m &= m - 1, ++at) {
+            const int j = j0 + __ffs(m) - 1;
+            if (here) {
+                sh.to[at] = j;
+                sh.to_row[at] = a.c.row(head, j);
+            } else if (KVP_CHECK(at >= 0 && at < a.B, 701, head, at)) {
+                to[at] = j;
+            }
+        }
+        at = kept_high;
+        for (uint32_t m = kept & ~low; m; m &= m - 1, ++at) {
+            const int j = j0 + __ffs(m) - 1;
+            if (here) sh.from[at] = j;
+            else if (KVP_CHECK(at < a.B, 702, head, at)) from[at] = j;
+        }
+        if (!fill) {
+            // evict_move fills in src and acc_out of the rows that stay: a bit each
+            const uint32_t stays = low & (kept | first_bits(s));
+            if (j0 < split) {
+                if (kPer == 16) ((uint16_t*)a.stays)[((size_t)head * a.stays_stride + j0 / 8) / 2] = (uint16_t)stays;
+                else a.stays[(size_t)head * a.stays_stride + j0 / 8] = (uint8_t)stays;
+            }
+        }
+        if (j0 <= t && t < j0 + kPer)                    // row t is this thread's
+            a.info[head] = make_int4(n, t, listed, here ? 0 : 1 + kept_high + __popc(kept & ~low & first_bits(t)));
+        if (rank == 0 && tid == 0) a.lens_out[head] = t;
+        // (the cluster's CTAs write into one another's shared memory only before the last sync_all)
     }
-    if (j0 <= t && t < j0 + kPer)                    // row t is this thread's
-        a.info[head] = make_int4(n, t, listed, here ? 0 : 1 + kept_high + __popc(kept & ~low & first_bits(t)));
-    if (rank == 0 && tid == 0) a.lens_out[head] = t;
-    // (the cluster's CTAs write into one another's shared memory only before the last sync_all)
     if (here) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
@@ -777,7 +846,9 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
     const int round = chunk * (kMoveThreads / 32);
     const int filled = fill ? std::min(e.budget, cap) : 0;
     const int want = std::max((most + round - 1) / round, (filled + kMoveThreads * 4 - 1) / (kMoveThreads * 4));
-    const int parts = std::max(1, std::min(want, sms * kMoveCtas / heads - 1));
+    // one wave of blocks for few heads; for many, whose share of a wave would be a block or less, four
+    const int wave = sms * kMoveCtas;
+    const int parts = std::max(1, std::min(want, heads * 4 <= wave ? wave / heads - 1 : (4 * wave + heads - 1) / heads));
     return s.head_dim == 128 ? launch_dependent(evict_move<128>, heads * (parts + 1), kMoveThreads, 0, st, a, parts, chunk, fill)
                              : launch_dependent(evict_move<64>, heads * (parts + 1), kMoveThreads, 0, st, a, parts, chunk, fill);
 }
