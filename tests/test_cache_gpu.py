@@ -171,6 +171,30 @@ def test_evict_sizes(b, hkv, rows, budget, spread):
     run_evict(c, budget, 4, 32, in_place=True)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("d,page,budget,window,over", [(64, 16, 150, 8, 150), (128, 32, 100, 0, 40), (128, 64, 90, 90, 300),
+                                                       (128, 16, 700, 32, 352), (64, 256, 40, 5, 400)])
+def test_evict_many_heads(d, page, budget, window, over, in_place):
+    """Heads enough to fill the card copy their rows themselves, up to some hundreds of them."""
+    lens = [budget + over * i // 151 for i in range(152)]
+    run_evict(Cache(d + over, 38, 4, 4, d, page, lens), budget, 2 if window < budget else 0, window, in_place=in_place)
+
+
+@pytest.mark.parametrize("equal", [False, True])
+def test_evict_a_few_rows(equal):
+    """Up to about ten rows over the budget, tied and not, absent pages among them."""
+    c = Cache(13, 3, 4, 4, 64, 16, [65, 66, 67, 68, 69, 70, 71, 72, 73, 74, 64, 0])
+    if equal:
+        c.acc[:] = torch.where(torch.arange(c.acc.numel()).view_as(c.acc) % 2 == 0, 1.0, 0.0)
+    run_evict(c, 64, 2, 5)
+    c.table[0, 1, 1], c.table[1, 2, 4] = -1, c.num_pages
+    c.k[:], c.v[:], c.acc[:] = (torch.nan_to_num(t) for t in (c.k, c.v, c.acc))
+    run_evict(c, 64, 2, 5, in_place=True)
+    run_evict(c, 64, 0, 64, in_place=True)
+    run_evict(c, 64, 64, 0)
+    run_evict(c, 60, 0, 0, budgets=[64, 60, 59, 60, 1, 60, 63, 60, 61, 60, 60, 2])
+
+
 @pytest.mark.parametrize("fill", ["equal", "zeros", "two", "nan", "negative", "inf", "near"])
 def test_evict_ties_and_odd_weights(fill):
     c = Cache(9, 2, 2, 2, 64, 16, [300, 65, 640, 513])

@@ -40,7 +40,10 @@ constexpr int kSliceCap = 48 * 1024;     // keys a CTA of evict_select_long hold
 constexpr int kManyThreads = 384;         // most threads of the CTAs that share an SM with others
 constexpr int kPerMost = 16;             // keys a thread of evict_select holds
 constexpr int kMoveThreads = 256, kMoveCtas = 3;   // of evict_move: threads, CTAs an SM
-constexpr int kMoveLoads = 8;            // 16-byte loads a lane of evict_move has in flight
+constexpr int kMoveLoads = 8;            // 16-byte loads a lane of evict_move has in flight,
+constexpr int kOwnLoads = 4;             // and of evict_select, where it copies rows itself:
+constexpr int kOwn = 384;                // past t - w up to as many, where there are heads enough to fill the card
+                                         // (512 heads of 2176 rows to 2048: 25 us, 34 by evict_move)
 constexpr int kLight = 8;                // rows given up up to which evict_select picks them one by one, and
 constexpr int kFew = 64;                 // rows past t - w up to which evict_select copies them itself (one CTA a head)
 
@@ -61,6 +64,7 @@ struct EvictArgs {
     uint8_t* stays;           // [heads][stays_stride]: a bit a row below t - w that keeps its place (clusters of evict_select)
     size_t stays_stride;
     int row_chunks;           // d / 8
+    bool many;                // heads enough to fill the card
     int slice;                // evict_select_long: keys that shared memory holds per CTA; 0: read again each round
 };
 
@@ -399,6 +403,18 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move(const Evic
     }
 }
 
+// The listed rows, then the window, by one CTA.
+template <int D>
+__device__ __forceinline__ void own_moves(const EvictArgs& a, int head, int n, int t, int listed, const int* from, const int* to) {
+    constexpr int kBatch = batch_rows<D>(kOwnLoads);
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, w = a.w;
+    move_rows<D, kOwnLoads, false>(a, head, 0, listed, warps * kBatch, kBatch, warp,
+                                   [&](int i) { return make_int2(from[i], to[i]); });
+    __syncthreads();
+    move_rows<D, kOwnLoads, true>(a, head, 0, w, warps * kBatch, kBatch, warp,
+                                  [&](int i) { return make_int2(n - w + i, t - w + i); });
+}
+
 constexpr int kBins = 256;
 
 template <int C>
@@ -414,7 +430,7 @@ struct PickShared {
     int above;
     bool exact;
     int listed;
-    int from[kFew], to[kFew];                        // listed rows, where they are copied here;
+    int from[C == 1 ? kOwn : 1], to[C == 1 ? kOwn : 1];   // listed rows, where they are copied here;
     long long to_row[kFew];                          // where the places lie in the pool;
     long long row[kFew];                             // rows [t - w, n): where they lie (-1: no page),
     float weight[kFew];                              // and their weights
@@ -535,6 +551,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
     int32_t* from = a.from + (size_t)head * a.B;
     int32_t* to = a.to + (size_t)head * a.B;
     int listed = 0;
+    const bool own = here || (C == 1 && a.many && n - split <= kOwn);   // this CTA copies the rows
     if (here && n - t <= kLight) {
         // ---- the n - t rows that go, one by one: the smallest key, of equal ones the highest row
         const int gone = n - t;
@@ -710,9 +727,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
         int at = max(0, min(j0, n - w) - s) - kept_low;
         for (uint32_t m = cand & low & ~kept; m; m &= m - 1, ++at) {
             const int j = j0 + __ffs(m) - 1;
-            if (here) {
+            if (own) {
                 sh.to[at] = j;
-                sh.to_row[at] = a.c.row(head, j);
+                if (here) sh.to_row[at] = a.c.row(head, j);
             } else if (KVP_CHECK(at >= 0 && at < a.B, 701, head, at)) {
                 to[at] = j;
             }
@@ -720,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
         at = kept_high;
         for (uint32_t m = kept & ~low; m; m &= m - 1, ++at) {
             const int j = j0 + __ffs(m) - 1;
-            if (here) sh.from[at] = j;
+            if (own) sh.from[at] = j;
             else if (KVP_CHECK(at < a.B, 702, head, at)) from[at] = j;
         }
         if (!fill) {
@@ -732,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
             }
         }
         if (j0 <= t && t < j0 + kPer)                    // row t is this thread's
-            a.info[head] = make_int4(n, t, listed, here ? 0 : 1 + kept_high + __popc(kept & ~low & first_bits(t)));
+            a.info[head] = make_int4(n, t, listed, own ? 0 : 1 + kept_high + __popc(kept & ~low & first_bits(t)));
         if (rank == 0 && tid == 0) a.lens_out[head] = t;
         // (the cluster's CTAs write into one another's shared memory only before the last sync_all)
     }
@@ -753,6 +770,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
             if (lane < 2 * chunks) pool[to_row * chunks] = ((const uint4*)keys)[r * 2 * chunks + lane];
             if (lane == 0) a.acc_out[to_row] = sh.weight[r];
         }
+    } else if (own) {
+        __syncthreads();
+        if (a.row_chunks == 16) own_moves<128>(a, head, n, t, listed, sh.from, sh.to);
+        else own_moves<64>(a, head, n, t, listed, sh.from, sh.to);
     }
 }
 
@@ -814,6 +835,7 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
     a.stays_stride = stays_stride(s);
     a.slice = 0;
     a.row_chunks = s.head_dim / 8;
+    a.many = heads >= num_sms();
     // CTAs per head: 8 where the heads alone would leave most SMs idle and rows are many
     const int sms = num_sms();
     const int C = cap > 4096 && (heads * 2 < sms || cap > kMaxThreads * kPerMost) ? 8 : 1;
@@ -822,9 +844,9 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
     bool fill = false;
     if (slice <= kMaxThreads * kPerMost) {
         // a cluster, whose CTAs have an SM each: 8 keys a thread, 16 once that takes more than 1024
-        // threads; else 16, for several CTAs an SM
+        // threads; else 16, for several CTAs an SM. 256 threads at least: they copy rows too.
         const int per = slice <= (C == 8 ? kMaxThreads : kManyThreads) * 8 ? 8 : kPerMost;
-        const int threads = std::max(64, (slice + per * 32 - 1) / (per * 32) * 32);
+        const int threads = std::max(256, (slice + per * 32 - 1) / (per * 32) * 32);
         if (C == 8) {
             err = launch_heads(per == 8 ? evict_select<8, 8> : evict_select<8, kPerMost>, a, C, threads, 0, st);
             fill = true;
@@ -838,7 +860,8 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
     }
     if (err != cudaSuccess) return err;
     // rows that can change places per head; blocks enough to fill the card with them
-    if (C == 1 && !budgets && cap - e.budget + e.window <= kFew) return cudaSuccess;   // evict_select copies them all
+    // evict_select copies them all where a head can have but few
+    if (C == 1 && !budgets && cap - e.budget + e.window <= (a.many ? kOwn : kFew)) return cudaSuccess;
     const int most = std::min(e.budget, std::max(0, cap - e.budget));
     // rows a warp takes at a time: 32, fewer where that would leave warps without any
     const int warps = sms * kMoveCtas * (kMoveThreads / 32), batch = s.head_dim == 128 ? batch_rows<128>(kMoveLoads) : batch_rows<64>(kMoveLoads);
