@@ -45,7 +45,8 @@ constexpr int kCtasPerSm = 2;
 constexpr int kResident = kPlanGrid * kCtasPerSm;
 constexpr int kMaxGrid = 2 * kResident;           // the workspace holds parts for as many CTAs
 constexpr int kLongRun = 32;                      // tiles of a run from which runs of unequal speed are balanced
-constexpr int kShortRun = 6;                      // and tiles of the short runs that do it
+constexpr int kShortRun = 6;                      // and tiles of the short runs that do it, at least
+constexpr int kMinRun = 4, kManyParts = 128;      // tiles of a run, at least, where a unit would have more parts
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinPieces = 2;                    // blocks of attend_join that weigh one share, at most
 constexpr int kCluster = 8;                       // CTAs of attend_short for a head,
@@ -95,13 +96,16 @@ __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kT
 // that lie nearer to the memory finish up to an eighth earlier than the rest, so of long runs the
 // last eighth of the tiles is left to `more` CTAs with short ones, which the hardware starts where
 // a CTA has ended. (24 caches of 0 to 16383 rows, GQA-7: 86 us, 87 without; 64 of 8192: 361, 377.)
+// Where few units would be cut into very many parts of very few tiles, whose join then takes longer
+// than their rows, fewer CTAs take part. (One head of 32768 rows: 14.0 us, 19.4 without; G 16: 20.5, 30.8.)
 struct Cutting {
     long long T, B;          // tiles; those of the first CTAs
     int first, more;
 
-    __device__ __forceinline__ Cutting(long long tiles, int resident, int grid) {
+    __device__ __forceinline__ Cutting(long long tiles, int units, int resident, int grid) {
         T = B = tiles;
         first = (int)min(T, (long long)resident);
+        if (first / units > kManyParts && T < (long long)kMinRun * first) first = (int)((T + kMinRun - 1) / kMinRun);
         more = 0;
         if (grid > resident && T >= (long long)kLongRun * resident) {
             more = (int)min((long long)(grid - resident), T / 8 / kShortRun);
@@ -261,7 +265,7 @@ __device__ __forceinline__ Cutting find_start(const CacheView& c, int ng, int re
         if (w < warp) before += warp_sums[w];
         T += warp_sums[w];
     }
-    const Cutting cutting(T, resident, gridDim.x);
+    const Cutting cutting(T, c.heads * ng, resident, gridDim.x);
     long long from = before + inc - sum;
     const long long want = (int)blockIdx.x < cutting.ctas() ? cutting.begin(blockIdx.x) : -1;
     if (want >= from && want < from + sum) {
@@ -337,7 +341,7 @@ __device__ __forceinline__ Cutting find_start_32(const CacheView& c, int ng, int
         const int y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
     }
-    const Cutting cutting(__shfl_sync(0xffffffffu, inc, 31), resident, gridDim.x);
+    const Cutting cutting(__shfl_sync(0xffffffffu, inc, 31), c.heads * ng, resident, gridDim.x);
     const int want = (int)cutting.begin(min((int)blockIdx.x, cutting.ctas()));
     const unsigned past = __ballot_sync(0xffffffffu, inc > want);
     const int head = past ? __ffs(past) - 1 : 0;
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
                 x.tile = tile;
                 x.count = step - seg_step + 1;
                 x.len = a.c.len(head);
-                const long long first = r0 + seg_step - tile;          // the unit's first tile in the run
+                const long long first = r0 + seg_step - tile;          // the unit's first tile of all
                 x.c0 = cutting.owner(first);
                 x.n = cutting.owner(first + tiles_of(x.len) - 1) - x.c0 + 1;
                 x.later = cutting.begin(x.c0) < first;
