@@ -8,13 +8,13 @@
 //
 // evict_select (up to 16 K rows a CTA): one CTA, or a cluster of 8, per head, each thread holding the
 // keys of kPer consecutive rows in registers. Eight bits of T a round, by a histogram in shared
-// memory; a cluster's CTAs write theirs into one another's shared memory. Every warp finds the
-// digit by itself, so that a round has one barrier (and one of the cluster). It ends as soon as
-// all keys that share T's bits stay. One scan of packed counts then gives every thread its places
-// in the lists. A head with few rows to copy is finished here; one that gives up few rows (a decode's
-// step: one) has them picked one by one instead, by every warp the lightest of its own rows and then by one
-// warp of all of those. (512 heads that give up one row of 2049: 7.2 us, 11.5 by rounds; rounds are
-// as fast from about 10 rows on.)
+// memory that one warp scans; a cluster's CTAs write theirs into one another's shared memory (a round of
+// a cluster takes 1.4 us, half of it the cluster's barrier). It ends as soon as all keys that share T's bits
+// stay. One scan of packed counts then gives every thread its places in the lists. A head with few
+// rows to copy is finished here; one that gives up few rows (a decode's step: one) has them picked
+// one by one instead, by every warp the lightest of its own rows and then by one warp of all of
+// those. (512 heads that give up one row of 2049: 7.2 us, 11.5 by rounds; rounds are as fast from
+// about 10 rows on.)
 // (Two bits a round by counting keys against three candidates, with no atomics: 28 us where this
 // takes 17 for 512 heads of 2064 rows.)
 // evict_select_long: longer rows, keys in shared memory or read again each round, four bits a round by
@@ -453,6 +453,25 @@ __device__ __forceinline__ unsigned long long warp_inclusive(unsigned long long 
     return x;
 }
 
+// A warp lists its rows: put(i, j) for each of them, j ascending, i from this thread's `at` on for its own.
+// bits: of rows [j0, j0 + kPer). 32 rows at a time, so that a warp's entries lie side by side (a
+// thread that writes its own rows' touches a sector each: 8 heads of 131072 rows: 65 us, 61.5 so).
+template <int kPer, typename Put>
+__device__ __forceinline__ void list_rows(uint32_t bits, int at, int j0, Put put) {
+    constexpr int kShare = 32 / kPer;                // threads that have 32 rows
+    if (!__any_sync(0xffffffffu, bits)) return;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < kShare; o <<= 1) bits |= __shfl_down_sync(0xffffffffu, bits, o) << (o * kPer);
+    j0 = __shfl_sync(0xffffffffu, j0, 0) + lane;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const uint32_t word = __shfl_sync(0xffffffffu, bits, q * kShare);
+        const int first = __shfl_sync(0xffffffffu, at, q * kShare);
+        if (word >> lane & 1) put(first + __popc(word & ((1u << lane) - 1)), j0 + 32 * q);
+    }
+}
+
 template <int C, int kPer, int kThreads = kMaxThreads, int kCtas = 1>
 __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs a) {
     extern __shared__ __align__(16) uint32_t keys[];   // (C = 1) rows [t - w, n), where they are few
@@ -679,13 +698,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
         }
         // rows whose key is T that stay, lowest first; none is needed where just kk keys reach T
         const int need_eq = exact ? 0 : kk - above;
+        const uint32_t over = exact ? T - 1 : T;     // (T > 0 where just kk reach it: all candidates, which are more, reach 0)
         uint32_t gt = 0, eqm = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            gt |= (exact ? key[i] >= T : key[i] > T) ? 1u << i : 0u;
-            eqm |= key[i] == T ? 1u << i : 0u;
+        for (int i = 0; i < kPer; ++i) gt |= key[i] > over ? 1u << i : 0u;
+        if (!exact) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) eqm |= key[i] == T ? 1u << i : 0u;
         }
-        if (exact) eqm = 0;
 
         // ---- places in the lists: counts before this thread's rows
         const unsigned long long mine = pack4(__popc(gt & low), __popc(eqm & low), __popc(gt & ~low), __popc(eqm & ~low));
@@ -725,20 +745,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
         const uint32_t kept = gt | eqm;
         // evicted places: candidates before this thread's rows less those kept
         int at = max(0, min(j0, n - w) - s) - kept_low;
-        for (uint32_t m = cand & low & ~kept; m; m &= m - 1, ++at) {
-            const int j = j0 + __ffs(m) - 1;
-            if (own) {
+        uint32_t out_low = cand & low & ~kept, in_high = kept & ~low;
+        const int early = kept_high + __popc(in_high & first_bits(t));       // listed rows below t, if row t is this thread's
+        if (own) {
+            for (; out_low; out_low &= out_low - 1, ++at) {
+                const int j = j0 + __ffs(out_low) - 1;
                 sh.to[at] = j;
                 if (here) sh.to_row[at] = a.c.row(head, j);
-            } else if (KVP_CHECK(at >= 0 && at < a.B, 701, head, at)) {
-                to[at] = j;
             }
-        }
-        at = kept_high;
-        for (uint32_t m = kept & ~low; m; m &= m - 1, ++at) {
-            const int j = j0 + __ffs(m) - 1;
-            if (own) sh.from[at] = j;
-            else if (KVP_CHECK(at < a.B, 702, head, at)) from[at] = j;
+            at = kept_high;
+            for (; in_high; in_high &= in_high - 1, ++at) sh.from[at] = j0 + __ffs(in_high) - 1;
+        } else {
+            list_rows<kPer>(out_low, at, j0, [&](int i, int j) { if (KVP_CHECK(i >= 0 && i < a.B, 701, head, i)) to[i] = j; });
+            list_rows<kPer>(in_high, kept_high, j0, [&](int i, int j) { if (KVP_CHECK(i >= 0 && i < a.B, 702, head, i)) from[i] = j; });
         }
         if (!fill) {
             // evict_move fills in src and acc_out of the rows that stay: a bit each
@@ -749,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
             }
         }
         if (j0 <= t && t < j0 + kPer)                    // row t is this thread's
-            a.info[head] = make_int4(n, t, listed, own ? 0 : 1 + kept_high + __popc(kept & ~low & first_bits(t)));
+            a.info[head] = make_int4(n, t, listed, own ? 0 : 1 + early);
         if (rank == 0 && tid == 0) a.lens_out[head] = t;
         // (the cluster's CTAs write into one another's shared memory only before the last sync_all)
     }
