@@ -91,6 +91,35 @@ def test_real_lengths(b, hq, hkv, d, page, lens):
     check(c, attend(c))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("b,hq,hkv,d,page,lens", [
+    (1, 8, 1, 128, 64, [50000]),                                  # more parts than a warp reads at a time
+    (1, 1, 1, 64, 16, [4160]),                                    # fewer than the eight joining blocks would have each
+    (1, 16, 1, 64, 16, [9001]),
+    (1, 40, 1, 128, 32, [12345]),                                 # three units, the last of 8 query heads
+    (1, 64, 1, 64, 256, [30000]),
+    (2, 24, 2, 128, 16, [0, 70, 20000, 4097]),                    # none, one tile, some cut
+    (4, 5, 1, 64, 128, [1, 0, 64, 12000]),
+    (1, 66, 2, 64, 64, [4200, 200]),                              # six units: more than few
+])
+def test_few_heads_over_the_card(b, hq, hkv, d, page, lens, dtype):
+    c = Cache(b + hq, b, hq, hkv, d, page, lens, dtype)
+    check(c, attend(c))
+    out, lse, _ = attend(c, acc=False)
+    check(c, (out, lse, None))
+
+
+@pytest.mark.parametrize("hq", [2, 34])
+def test_a_workspace_used_again_with_other_lengths(hq):
+    """What a call wrote of the units it cut is not taken for the next call's."""
+    m = kvp()
+    c = Cache(hq, 1, hq, 2, 64, 32, [20000, 20000])
+    ws = m.attend_workspace_for(c.shape, True)
+    for lens in ([20000, 6000], [64, 6000], [0, 0], [20000, 0], [5, 40], [3000, 20000]):
+        at = torch.tensor([lens], dtype=torch.int32)
+        check(c, attend(c, lens=at.cuda(), workspace=ws), lens=at)
+
+
 @both
 def test_all_heads_empty(long_table):
     c = Cache(1, 3, 8, 2, 64, 16, [0] * 6, width=width_of(long_table, 16))

@@ -15,13 +15,13 @@
 // are joined in shared memory; a unit that lies within one CTA is finished, others leave a part
 // (unnormalised output, maximum, sum) in the workspace.
 // attend_join: joins the parts of the units that were cut (a CTA has two at most), in the order of
-// the rows.
+// the rows. attend_join_few: the same where units are few and have very many parts.
 // attend_short (few heads with short caches, as an eviction leaves them): a cluster of 8 CTAs a head,
 // one launch. All of a head's rows are in flight at once; the CTAs' parts are joined through
 // distributed shared memory and the logits never leave the SM.
 // The weights that acc gains need the final sum, so the logits go through the workspace (4 G bytes
 // a row against 4 d of the row itself) and are read back, mostly from L2, by the CTA that finished
-// the unit, or by attend_join for units that were cut.
+// the unit, or by attend_join for units that were cut (attend_weigh, where units are few or a head's several).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -46,10 +46,10 @@ constexpr int kResident = kPlanGrid * kCtasPerSm;
 constexpr int kMaxGrid = 2 * kResident;           // the workspace holds parts for as many CTAs
 constexpr int kLongRun = 32;                      // tiles of a run from which runs of unequal speed are balanced
 constexpr int kShortRun = 6;                      // and tiles of the short runs that do it, at least
-constexpr int kMinRun = 4, kManyParts = 128;      // tiles of a run, at least, where a unit would have more parts
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinPieces = 2;                    // blocks of attend_join that weigh one share, at most
-constexpr int kCluster = 8;                       // CTAs of attend_short for a head,
+constexpr int kFewUnits = 4;                      // units up to which a cluster joins each query head
+constexpr int kCluster = 8;                       // its CTAs, and those of attend_short for a head,
 constexpr int kShortWarps = 8, kShortThreads = kShortWarps * 32;
 constexpr int kShortRows = 512;                   // rows each may have,
 constexpr int kShortCtas = 120;                   // and CTAs in all: 15 clusters of 8 SMs find room on 148
@@ -84,9 +84,10 @@ struct AttendArgs {
     float scale2;        // log2 e / sqrt(d)
     // workspace
     Cut* cuts;           // [2 grid]: what each CTA's first and last unit had of it, where they were cut
+    Cut* firsts;         // [units]: a cut unit's first share (unit = -1: not cut); NULL with more than kFewUnits units
     float2* stats;       // [2 grid][gq]: a part's maximum and sum, log2 domain
     float* parts;        // [2 grid][gq][d]: a part's unnormalised output
-    float* lse2;         // [heads * G], with acc and more than one unit a head
+    float* lse2;         // [heads * G], where attend_weigh adds the weights (acc, and more than one unit a head or firsts)
     float* logits;       // [heads * G][cap]: q . k; NULL without acc
 };
 
@@ -96,16 +97,13 @@ __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kT
 // that lie nearer to the memory finish up to an eighth earlier than the rest, so of long runs the
 // last eighth of the tiles is left to `more` CTAs with short ones, which the hardware starts where
 // a CTA has ended. (24 caches of 0 to 16383 rows, GQA-7: 86 us, 87 without; 64 of 8192: 361, 377.)
-// Where few units would be cut into very many parts of very few tiles, whose join then takes longer
-// than their rows, fewer CTAs take part. (One head of 32768 rows: 14.0 us, 19.4 without; G 16: 20.5, 30.8.)
 struct Cutting {
     long long T, B;          // tiles; those of the first CTAs
     int first, more;
 
-    __device__ __forceinline__ Cutting(long long tiles, int units, int resident, int grid) {
+    __device__ __forceinline__ Cutting(long long tiles, int resident, int grid) {
         T = B = tiles;
         first = (int)min(T, (long long)resident);
-        if (first / units > kManyParts && T < (long long)kMinRun * first) first = (int)((T + kMinRun - 1) / kMinRun);
         more = 0;
         if (grid > resident && T >= (long long)kLongRun * resident) {
             more = (int)min((long long)(grid - resident), T / 8 / kShortRun);
@@ -265,7 +263,7 @@ __device__ __forceinline__ Cutting find_start(const CacheView& c, int ng, int re
         if (w < warp) before += warp_sums[w];
         T += warp_sums[w];
     }
-    const Cutting cutting(T, c.heads * ng, resident, gridDim.x);
+    const Cutting cutting(T, resident, gridDim.x);
     long long from = before + inc - sum;
     const long long want = (int)blockIdx.x < cutting.ctas() ? cutting.begin(blockIdx.x) : -1;
     if (want >= from && want < from + sum) {
@@ -341,7 +339,7 @@ __device__ __forceinline__ Cutting find_start_32(const CacheView& c, int ng, int
         const int y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
     }
-    const Cutting cutting(__shfl_sync(0xffffffffu, inc, 31), c.heads * ng, resident, gridDim.x);
+    const Cutting cutting(__shfl_sync(0xffffffffu, inc, 31), resident, gridDim.x);
     const int want = (int)cutting.begin(min((int)blockIdx.x, cutting.ctas()));
     const unsigned past = __ballot_sync(0xffffffffu, inc > want);
     const int head = past ? __ffs(past) - 1 : 0;
@@ -621,6 +619,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
         if (a.c.len(h) > 0) continue;
         for (int e = tid; e < a.G * D; e += kThreads) ((T*)a.out)[(size_t)h * a.G * D + e] = T(0.f);
         if (a.lse && tid < a.G) a.lse[(size_t)h * a.G + tid] = -INFINITY;
+        if (a.firsts && tid < a.ng) a.firsts[h * a.ng + tid].unit = -1;
     }
     if (tid < 2) a.cuts[2 * cta + tid].unit = -1;
     if (cta >= cutting.ctas()) return;
@@ -749,8 +748,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
                 x.n = cutting.owner(first + tiles_of(x.len) - 1) - x.c0 + 1;
                 x.later = cutting.begin(x.c0) < first;
                 a.cuts[slot] = x;
+                if (a.firsts && tile == 0) a.firsts[x.unit] = x;
             }
-            if (whole && a.logits && a.ng == 1)
+            if (whole && a.firsts && tid == 0) a.firsts[head * a.ng + m.sub].unit = -1;
+            if (whole && a.logits && !a.lse2)
                 add_weights<kThreads>(a, head, 0, a.c.len(head), tid, sh_lse2);
             segment = 1;
         }
@@ -1005,7 +1006,79 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendArgs 
     }
 }
 
-// acc += the weights, for heads whose query heads are several units (G > 16): `per` blocks a head,
+// The outputs of few units, whose parts are many: a cluster a query head, an eighth of its parts a CTA. (attend_weigh
+// then adds the weights.) One head of 131072 rows: G 8 18.2 us, 28.5 by attend_join; G 16 19.5, 37.4; with acc 22.3
+// and 25.0, 28.1 and 39.8 by attend_join, whose every weighing block adds up the parts' sums again.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads, 2) attend_join_few(const AttendArgs a, int rows) {
+    constexpr int kAhead = 5, kCols = D / 32;
+    using Piece = typename std::conditional<kCols == 4, float4, float2>::type;
+    __shared__ __align__(16) float warp_part[kJoinWarps][D], cta_part[D];
+    __shared__ float2 warp_stat[kJoinWarps], cta_stat;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, join = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
+    const Cut p = a.firsts[join / rows];
+    const int row = join % rows, g0 = p.unit < 0 ? 0 : (p.unit - p.head * a.ng) * a.gq;
+    if (p.unit < 0 || g0 + row >= a.G) return;                  // the whole cluster
+    float top = kLowest, l = 0.f, val[kCols] = {};
+    const int last = p.n * (rank + 1) / kCluster;
+    for (int base = p.n * rank / kCluster + warp; base < last; base += kAhead * kJoinWarps) {
+        float2 st[kAhead];
+        Piece y[kAhead];
+        float m = top;
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const int part = base + x * kJoinWarps;
+            st[x] = make_float2(kLowest, 0.f);
+            y[x] = Piece{};
+            if (part >= last) continue;
+            const size_t at = p.slot(part) * a.gq + row;
+            st[x] = a.stats[at];
+            y[x] = ((const Piece*)(a.parts + at * D))[lane];
+        }
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) m = fmaxf(m, st[x].x);
+        const float f = ptx::ex2(top - m);
+        l *= f;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) val[c] *= f;
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const float fx = ptx::ex2(st[x].x - m);
+            l += fx * st[x].y;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) val[c] += fx * ((const float*)&y[x])[c];
+        }
+        top = m;
+    }
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) warp_part[warp][lane * kCols + c] = val[c];
+    if (lane == 0) warp_stat[warp] = make_float2(top, l);
+    __syncthreads();
+    if (warp == 0) {
+        const float2 st = add_parts<D, kJoinWarps>(
+            val, [&](int x) { return warp_part[x] + lane * kCols; }, [&](int x) { return warp_stat[x]; });
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) cta_part[lane * kCols + c] = val[c];
+        if (lane == 0) cta_stat = st;
+    }
+    ptx::cluster_arrive();
+    ptx::cluster_wait();
+    if (rank == 0 && warp == 0) {
+        cg::cluster_group cluster = cg::this_cluster();
+        float2 st = add_parts<D, kCluster>(
+            val, [&](int x) { return (const float*)cluster.map_shared_rank(&cta_part[lane * kCols], x); },
+            [&](int x) { return *cluster.map_shared_rank(&cta_stat, x); });
+        st.x += Pair<T>::kBias;                                 // (taken off the parts' maxima)
+        put_output<T, D>(a, (size_t)p.head * a.G + g0 + row, val, st);
+    }
+    __syncwarp();
+    ptx::cluster_arrive();                                      // its shared memory outlives its readers
+    ptx::cluster_wait();
+}
+
+// acc += the weights, where units are few or a head's query heads are several (G > 16): `per` blocks a head,
 // once all of its sums are known.
 __global__ void __launch_bounds__(kJoinThreads) attend_weigh(const AttendArgs a, int per) {
     __shared__ float sh_lse2[kMaxCacheGroup];
@@ -1017,16 +1090,25 @@ __global__ void __launch_bounds__(kJoinThreads) attend_weigh(const AttendArgs a,
         sh_lse2[g] = x == -INFINITY ? INFINITY : x;
     }
     __syncthreads();
-    constexpr int kRows = kJoinThreads * 4;
-    for (int j = blockIdx.x % per * kRows; j < len; j += per * kRows)
-        add_weights<kJoinThreads>(a, head, j, min(len, j + kRows), threadIdx.x, sh_lse2);
+    const int cap = a.c.cap();
+    for (int j = blockIdx.x % per * kJoinThreads + threadIdx.x; j < len; j += per * kJoinThreads) {
+        const long long row = a.c.row(head, j);
+        if (row < 0) continue;
+        if (!KVP_CHECK(row < ((long long)a.c.num_pages << a.c.page_shift), 603, head, j)) continue;
+        const float* lp = a.logits + (size_t)head * a.G * cap + j;
+        const float drawn = a.acc[row];
+        float sum = 0.f;
+#pragma unroll 8
+        for (int g = 0; g < a.G; ++g) sum += ptx::ex2(fmaf(lp[(size_t)g * cap], a.scale2, -sh_lse2[g]));
+        a.acc[row] = drawn + sum;
+    }
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
     int ng, gq;
-    size_t cuts, stats, parts, lse2, logits, bytes;
+    size_t cuts, firsts, stats, parts, lse2, logits, bytes;
 };
 
 // bytes = 0: more tiles than the kernels count in 32 bits.
@@ -1044,10 +1126,11 @@ Layout layout_of(const kvp_cache_shape& s, bool accumulate) {
         return here;
     };
     l.cuts = take((size_t)2 * kMaxGrid * sizeof(Cut));
+    l.firsts = take(kFewUnits * sizeof(Cut));
     l.stats = take((size_t)2 * kMaxGrid * l.gq * sizeof(float2));
     l.parts = take((size_t)2 * kMaxGrid * l.gq * d * sizeof(float));
     if (accumulate) {
-        if (l.ng > 1) l.lse2 = take((size_t)heads * G * sizeof(float));
+        if (l.ng > 1 || heads <= kFewUnits) l.lse2 = take((size_t)heads * G * sizeof(float));
         l.logits = take((size_t)heads * G * cap * sizeof(float));
     }
     l.bytes = at;
@@ -1063,15 +1146,12 @@ cudaError_t launch_split(const AttendArgs& a, int grid, cudaStream_t st) {
     return launch_dependent(kernel, grid, kThreads, smem, st, a);
 }
 
-template <typename T, int D, bool kWide, int kStages>
-cudaError_t launch_short(const AttendArgs& a, cudaStream_t st) {
-    auto kernel = attend_short<T, D, kWide, kStages>;
-    constexpr size_t smem = Short<T, D, kWide, kStages>::kSmem;
-    const cudaError_t e = allow_dynamic_smem((const void*)kernel, smem);
-    if (e != cudaSuccess) return e;
+// launch_dependent, in clusters of kCluster CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), int grid, int block, size_t smem, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.c.heads * kCluster));
-    cfg.blockDim = dim3(kShortThreads);
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -1083,7 +1163,16 @@ cudaError_t launch_short(const AttendArgs& a, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
+}
+
+template <typename T, int D, bool kWide, int kStages>
+cudaError_t launch_short(const AttendArgs& a, cudaStream_t st) {
+    auto kernel = attend_short<T, D, kWide, kStages>;
+    constexpr size_t smem = Short<T, D, kWide, kStages>::kSmem;
+    const cudaError_t e = allow_dynamic_smem((const void*)kernel, smem);
+    if (e != cudaSuccess) return e;
+    return launch_clusters(kernel, a.c.heads * kCluster, kShortThreads, smem, st, a);
 }
 
 template <typename T, int D>
@@ -1106,11 +1195,12 @@ cudaError_t launch_all(AttendArgs a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const long long share = (most + a.resident - 1) / a.resident * kTile;       // rows of a share, at most
     const int pieces = (int)std::min<long long>(kJoinPieces, (share + kJoinThreads * 4 - 1) / (kJoinThreads * 4));
-    const int weighers = a.logits && a.ng == 1 ? 2 * (a.resident * pieces + more) : 0, rows = std::min(a.G, a.gq);
-    e = launch_dependent(attend_join<T, D>, weighers + (a.resident + more) * rows, kJoinThreads, 0, st, a, weighers, pieces,
-                         rows);
+    const int weighers = a.logits && !a.lse2 ? 2 * (a.resident * pieces + more) : 0, rows = std::min(a.G, a.gq);
+    e = a.firsts ? launch_clusters(attend_join_few<T, D>, a.c.heads * a.ng * rows * kCluster, kJoinThreads, 0, st, a, rows)
+                 : launch_dependent(attend_join<T, D>, weighers + (a.resident + more) * rows, kJoinThreads, 0, st, a,
+                                    weighers, pieces, rows);
     if (e != cudaSuccess || !a.lse2) return e;
-    const int per = std::max(1, std::min(num_sms() * 8 / a.c.heads, (a.c.cap() + kJoinThreads * 4 - 1) / (kJoinThreads * 4)));
+    const int per = std::max(1, std::min(num_sms() * 8 / a.c.heads, (a.c.cap() + kJoinThreads - 1) / kJoinThreads));
     return launch_dependent(attend_weigh, a.c.heads * per, kJoinThreads, 0, st, a, per);
 }
 
@@ -1136,9 +1226,10 @@ cudaError_t launch_attend(const kvp_cache_shape& s, const uint16_t* q, const uin
     a.gq = l.gq;
     a.scale2 = (float)(1.4426950408889634 / sqrt((double)s.head_dim));
     a.cuts = (Cut*)(ws + l.cuts);
+    a.firsts = (long long)a.c.heads * a.ng <= kFewUnits ? (Cut*)(ws + l.firsts) : nullptr;
     a.stats = (float2*)(ws + l.stats);
     a.parts = (float*)(ws + l.parts);
-    a.lse2 = acc && l.ng > 1 ? (float*)(ws + l.lse2) : nullptr;
+    a.lse2 = acc && (l.ng > 1 || a.firsts) ? (float*)(ws + l.lse2) : nullptr;
     a.logits = acc ? (float*)(ws + l.logits) : nullptr;
     if (s.dtype == KVP_BF16)
         return s.head_dim == 128 ? launch_all<__nv_bfloat16, 128>(a, st)
