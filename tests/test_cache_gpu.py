@@ -171,6 +171,15 @@ def test_evict_sizes(b, hkv, rows, budget, spread):
     run_evict(c, budget, 4, 32, in_place=True)
 
 
+@pytest.mark.parametrize("heads,rows,budget", [(20, 30000, 15000), (36, 10000, 9000), (37, 10000, 9000), (15, 60000, 800),
+                                               (18, 8192, 8000)])
+def test_evict_heads_and_clusters(heads, rows, budget):
+    """More clusters than run at once, and the numbers of heads and rows about which they are used."""
+    c = Cache(heads, heads, 1, 1, 64, 128, [rows - 3 * i for i in range(heads)])
+    run_evict(c, budget, 0, 16)
+    run_evict(c, budget, 5, 0, in_place=True)
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("d,page,budget,window,over", [(64, 16, 150, 8, 150), (128, 32, 100, 0, 40), (128, 64, 90, 90, 300),
                                                        (128, 16, 700, 32, 352), (64, 256, 40, 5, 400)])

@@ -37,6 +37,7 @@ namespace {
 constexpr int kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kSliceCap = 48 * 1024;     // keys a CTA of evict_select_long holds in shared memory
+constexpr int kClusters = 15;             // clusters of 8 CTAs with an SM each that run at once
 constexpr int kManyThreads = 384;         // most threads of the CTAs that share an SM with others
 constexpr int kPerMost = 16;             // keys a thread of evict_select holds
 constexpr int kMoveThreads = 256, kMoveCtas = 3;   // of evict_move: threads, CTAs an SM
@@ -855,16 +856,20 @@ cudaError_t launch_evict(const kvp_cache_shape& s, const kvp_evict& e, const int
     a.slice = 0;
     a.row_chunks = s.head_dim / 8;
     a.many = heads >= num_sms();
-    // CTAs per head: 8 where the heads alone would leave most SMs idle and rows are many
+    // CTAs per head: 8 where rows are many and heads few. (8 heads of 16384 rows: 15.0 us, 17.8 by a CTA each; 32: 37.3,
+    // 37.9; 72 of 12000: 39.0, 31.1; 32 of 8192: 28.9, 27.4; 8 of 8192: 13.5, 13.8.)
     const int sms = num_sms();
-    const int C = cap > 4096 && (heads * 2 < sms || cap > kMaxThreads * kPerMost) ? 8 : 1;
+    const int C = cap > 8192 && (heads * 4 < sms || cap > kMaxThreads * kPerMost) ? 8 : 1;
     const int slice = (cap + C - 1) / C;
     cudaError_t err;
     bool fill = false;
     if (slice <= kMaxThreads * kPerMost) {
-        // a cluster, whose CTAs have an SM each: 8 keys a thread, 16 once that takes more than 1024
-        // threads; else 16, for several CTAs an SM. 256 threads at least: they copy rows too.
-        const int per = slice <= (C == 8 ? kMaxThreads : kManyThreads) * 8 ? 8 : kPerMost;
+        // 8 keys a thread, or 16 where the threads that takes would keep other CTAs off their SM: a
+        // cluster's more than run at once (64 heads of 30000 rows: 65 us with 8, 59 with 16; 24 of 24000: 44.9, 46.4),
+        // a CTA's more than kManyThreads. 256 threads at least: they copy rows too.
+        const int with8 = std::max(256, (slice + 255) / 256 * 32);
+        const bool fit8 = C == 1 ? with8 <= kManyThreads : with8 <= 256 || heads <= kMaxThreads / with8 * kClusters;
+        const int per = fit8 ? 8 : kPerMost;
         const int threads = std::max(256, (slice + per * 32 - 1) / (per * 32) * 32);
         if (C == 8) {
             err = launch_heads(per == 8 ? evict_select<8, 8> : evict_select<8, kPerMost>, a, C, threads, 0, st);
