@@ -46,9 +46,11 @@ constexpr int kResident = kPlanGrid * kCtasPerSm;
 constexpr int kMaxGrid = 2 * kResident;           // the workspace holds parts for as many CTAs
 constexpr int kLongRun = 32;                      // tiles of a run from which runs of unequal speed are balanced
 constexpr int kShortRun = 6;                      // and tiles of the short runs that do it, at least
+constexpr int kMinRun = 4, kManyParts = 128;      // tiles of a run, at least, where a unit would have more parts
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinPieces = 2;                    // blocks of attend_join that weigh one share, at most
-constexpr int kFewUnits = 4;                      // units up to which a cluster joins each query head
+constexpr int kFewUnits = 4;                      // units up to which a cluster joins each query head,
+constexpr int kFewSteps = 6;                      // and steps of adding up their sums from which it does so with acc too
 constexpr int kCluster = 8;                       // its CTAs, and those of attend_short for a head,
 constexpr int kShortWarps = 8, kShortThreads = kShortWarps * 32;
 constexpr int kShortRows = 512;                   // rows each may have,
@@ -80,11 +82,12 @@ struct AttendArgs {
     float* lse;          // NULL: not wanted
     float* acc;          // NULL: not wanted
     int resident;        // CTAs of attend_split that run at once; the grid may have more
+    int many;            // CTAs from which their runs are not cut below kMinRun tiles
     int G, ng, gq;       // query heads per head; units per head; query heads per unit (the last: fewer)
     float scale2;        // log2 e / sqrt(d)
     // workspace
     Cut* cuts;           // [2 grid]: what each CTA's first and last unit had of it, where they were cut
-    Cut* firsts;         // [units]: a cut unit's first share (unit = -1: not cut); NULL with more than kFewUnits units
+    Cut* firsts;         // [units]: a cut unit's first share (unit = -1: not cut); NULL where units are not few
     float2* stats;       // [2 grid][gq]: a part's maximum and sum, log2 domain
     float* parts;        // [2 grid][gq][d]: a part's unnormalised output
     float* lse2;         // [heads * G], where attend_weigh adds the weights (acc, and more than one unit a head or firsts)
@@ -97,13 +100,16 @@ __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kT
 // that lie nearer to the memory finish up to an eighth earlier than the rest, so of long runs the
 // last eighth of the tiles is left to `more` CTAs with short ones, which the hardware starts where
 // a CTA has ended. (24 caches of 0 to 16383 rows, GQA-7: 86 us, 87 without; 64 of 8192: 361, 377.)
+// Where attend_join would have to join more than `many` parts of very few tiles, which takes longer than
+// their rows, fewer CTAs take part. (2 heads of 30000 rows, G 4, acc: 14.2 us, 15.2 without.)
 struct Cutting {
     long long T, B;          // tiles; those of the first CTAs
     int first, more;
 
-    __device__ __forceinline__ Cutting(long long tiles, int resident, int grid) {
+    __device__ __forceinline__ Cutting(long long tiles, int resident, int grid, int many) {
         T = B = tiles;
         first = (int)min(T, (long long)resident);
+        if (first > many && T < (long long)kMinRun * first) first = (int)((T + kMinRun - 1) / kMinRun);
         more = 0;
         if (grid > resident && T >= (long long)kLongRun * resident) {
             more = (int)min((long long)(grid - resident), T / 8 / kShortRun);
@@ -242,7 +248,7 @@ __device__ __forceinline__ void add_weights(const AttendArgs& a, int head, int j
 
 // Where tile `want` of the run lies: every thread of the CTA sums a stretch of heads' tiles, and
 // the one whose stretch holds `want` walks it. Sets *at (shared) and returns the total.
-__device__ __forceinline__ Cutting find_start(const CacheView& c, int ng, int resident, long long* warp_sums,
+__device__ __forceinline__ Cutting find_start(const CacheView& c, int ng, int resident, int many, long long* warp_sums,
                                               Start* at) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (c.heads + kThreads - 1) / kThreads;
@@ -263,7 +269,7 @@ __device__ __forceinline__ Cutting find_start(const CacheView& c, int ng, int re
         if (w < warp) before += warp_sums[w];
         T += warp_sums[w];
     }
-    const Cutting cutting(T, resident, gridDim.x);
+    const Cutting cutting(T, resident, gridDim.x, many);
     long long from = before + inc - sum;
     const long long want = (int)blockIdx.x < cutting.ctas() ? cutting.begin(blockIdx.x) : -1;
     if (want >= from && want < from + sum) {
@@ -329,7 +335,7 @@ struct Walk {
 
 // Of up to 32 heads every warp finds its CTA's run by itself, a length a lane, with no barrier and no
 // second read of the lengths.
-__device__ __forceinline__ Cutting find_start_32(const CacheView& c, int ng, int resident, Start* at, int* lane_len) {
+__device__ __forceinline__ Cutting find_start_32(const CacheView& c, int ng, int resident, int many, Start* at, int* lane_len) {
     const int lane = threadIdx.x & 31;
     *lane_len = lane < c.heads ? c.len(lane) : 0;
     const int nt = tiles_of(*lane_len), n = nt * ng;          // (at most 2^19 tiles each)
@@ -339,7 +345,7 @@ __device__ __forceinline__ Cutting find_start_32(const CacheView& c, int ng, int
         const int y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
     }
-    const Cutting cutting(__shfl_sync(0xffffffffu, inc, 31), resident, gridDim.x);
+    const Cutting cutting(__shfl_sync(0xffffffffu, inc, 31), resident, gridDim.x, many);
     const int want = (int)cutting.begin(min((int)blockIdx.x, cutting.ctas()));
     const unsigned past = __ballot_sync(0xffffffffu, inc > want);
     const int head = past ? __ffs(past) - 1 : 0;
@@ -610,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
     Start at;
     Walk w;
     const bool few = a.c.heads <= 32;
-    const Cutting cutting = few ? find_start_32(a.c, a.ng, a.resident, &at, &w.lane_len)
-                                : find_start(a.c, a.ng, a.resident, warp_sums, &sh_at);
+    const Cutting cutting = few ? find_start_32(a.c, a.ng, a.resident, a.many, &at, &w.lane_len)
+                                : find_start(a.c, a.ng, a.resident, a.many, warp_sums, &sh_at);
     if (!few) at = sh_at;
     ptx::launch_dependents();
     // heads without rows
@@ -1175,8 +1181,25 @@ cudaError_t launch_short(const AttendArgs& a, cudaStream_t st) {
     return launch_clusters(kernel, a.c.heads * kCluster, kShortThreads, smem, st, a);
 }
 
+// Tiles, at most.
+long long most_tiles(const AttendArgs& a) { return (long long)a.c.heads * a.ng * ((a.c.cap() + kTile - 1) / kTile); }
+
+// As many CTAs of attend_split as are resident at once, but no more than there can be tiles.
+int resident_ctas(const AttendArgs& a) {
+    return (int)std::min<long long>(most_tiles(a), std::min(num_sms(), kPlanGrid) * kCtasPerSm);
+}
+
+// Whether attend_join_few joins the units. With acc attend_weigh has to follow it (3 us), which pays where every weighing
+// block of attend_join would add up sums for longer: a warp ceil(G / 8) query heads, a lane every 32nd of a
+// unit's parts. (G 16, 296 parts, 20 steps: 39.8 us, 25.0 so; G 12, 94 parts, 6: 15.2, 13.6; G 4, 148 parts, 5: 13.4, 15.6.)
+bool joins_few(const AttendArgs& a) {
+    const int units = a.c.heads * a.ng;
+    if (units > kFewUnits) return false;
+    return !a.acc || a.ng > 1 || (a.G + kJoinWarps - 1) / kJoinWarps * ((a.resident / units + 31) / 32) >= kFewSteps;
+}
+
 template <typename T, int D>
-cudaError_t launch_all(AttendArgs a, cudaStream_t st) {
+cudaError_t launch_all(const AttendArgs& a, cudaStream_t st) {
     constexpr int kStages = D == 128 ? 3 : 6;
     // One launch where heads are so few that their clusters run at once, and no table holds more rows
     // than a cluster takes. (8 heads of 2111 rows: 6.6 us, 9.3 by
@@ -1185,10 +1208,8 @@ cudaError_t launch_all(AttendArgs a, cudaStream_t st) {
         if (a.gq == 16) return launch_short<T, D, true, D == 128 ? 2 : 4>(a, st);
         return launch_short<T, D, false, D == 128 ? 3 : 4>(a, st);
     }
-    // as many CTAs as are resident at once, but no more than there can be tiles, and as many with
-    // short runs where runs can be long
-    const long long most = (long long)a.c.heads * a.ng * ((a.c.cap() + kTile - 1) / kTile);
-    a.resident = (int)std::min<long long>(most, std::min(num_sms(), kPlanGrid) * kCtasPerSm);
+    // as many CTAs with short runs again where runs can be long
+    const long long most = most_tiles(a);
     const int more = most >= (long long)kLongRun * a.resident ? a.resident : 0;
     cudaError_t e = a.gq == 16 ? launch_split<T, D, true, kStages>(a, a.resident + more, st)
                                : launch_split<T, D, false, kStages>(a, a.resident + more, st);
@@ -1226,9 +1247,11 @@ cudaError_t launch_attend(const kvp_cache_shape& s, const uint16_t* q, const uin
     a.gq = l.gq;
     a.scale2 = (float)(1.4426950408889634 / sqrt((double)s.head_dim));
     a.cuts = (Cut*)(ws + l.cuts);
-    a.firsts = (long long)a.c.heads * a.ng <= kFewUnits ? (Cut*)(ws + l.firsts) : nullptr;
     a.stats = (float2*)(ws + l.stats);
     a.parts = (float*)(ws + l.parts);
+    a.resident = resident_ctas(a);
+    a.firsts = joins_few(a) ? (Cut*)(ws + l.firsts) : nullptr;
+    a.many = a.firsts ? INT_MAX : (int)std::min<long long>(INT_MAX, (long long)kManyParts * a.c.heads * a.ng);
     a.lse2 = acc && (l.ng > 1 || a.firsts) ? (float*)(ws + l.lse2) : nullptr;
     a.logits = acc ? (float*)(ws + l.logits) : nullptr;
     if (s.dtype == KVP_BF16)
