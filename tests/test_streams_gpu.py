@@ -1,0 +1,61 @@
+"""Calls that allocate their own scratch, on another stream than the current one, while the current
+stream still writes to a block of that size which was just given back."""
+import numpy as np
+import pytest
+import torch
+
+from tests.cache_utils import Cache, bits, kvp
+
+pytestmark = pytest.mark.gpu
+
+
+def busy(nbytes):
+    """The current stream's allocator gets a block of `nbytes` back that its queue writes to yet."""
+    block = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    torch.cuda._sleep(20_000_000)
+    for _ in range(20):
+        block.fill_(0x7F)
+
+
+STREAMS = {"stream": lambda s: s, "handle": lambda s: s.cuda_stream, "default": lambda s: 0, "none": lambda s: None}
+
+
+@pytest.mark.parametrize("given", STREAMS)
+@pytest.mark.parametrize("width", [None, 300])
+def test_attend(given, width):
+    m = kvp()
+    c = Cache(1, 1, 8, 2, 64, 16, [900, 333], width=width)
+    side = torch.cuda.Stream()
+    n = m.attend_workspace_for(c.shape, True).numel()
+    got = []
+    for stream in (None, STREAMS[given](side)):
+        q, k, v, table, lens, acc = c.gpu("q", "k", "v", "table", "lens", "acc")
+        out, lse = torch.empty_like(q), torch.empty((c.b, c.hq), device="cuda")
+        torch.cuda.synchronize()
+        if stream is not None:
+            busy(n)
+        m.kvp_cache_attend(c.shape, q, k, v, table, lens, out, lse, acc, stream=stream)
+        torch.cuda.synchronize()
+        got.append([bits(t) for t in (out, lse, acc)])
+    for x, y in zip(*got):
+        assert np.array_equal(x, y)
+
+
+@pytest.mark.parametrize("given", STREAMS)
+@pytest.mark.parametrize("rows,budget", [(900, 400), (9000, 5000)])
+def test_evict(given, rows, budget):
+    m = kvp()
+    c = Cache(2, 1, 2, 2, 64, 16, [rows, rows - 9])
+    side, ev = torch.cuda.Stream(), m.make_evict(budget, 4, 16)
+    n = m.evict_workspace_for(c.shape, ev).numel()
+    got = []
+    for stream in (None, STREAMS[given](side)):
+        k, v, acc, table, lens = c.gpu("k", "v", "acc", "table", "lens")
+        torch.cuda.synchronize()
+        if stream is not None:
+            busy(n)
+        m.kvp_cache_evict(c.shape, ev, k, v, acc, acc, table, lens, lens, stream=stream)
+        torch.cuda.synchronize()
+        got.append([bits(t) for t in (k, v, acc, lens)])
+    for x, y in zip(*got):
+        assert np.array_equal(x, y)

@@ -34,6 +34,7 @@ importing this package raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -230,6 +231,19 @@ def _stream(stream):
     return int(stream)
 
 
+def _current(stream, device):
+    """`stream`, as the calls take it, made current for as long as the result is entered. What a call
+    allocates for itself is allocated in it: the caching allocator then hands out no block that work
+    on another stream still uses, and reuses the block behind the call's own work."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        # (0 and 1 are the default stream's handles, not those of a stream made elsewhere)
+        stream = (torch.cuda.default_stream(device) if int(stream) in (0, 1)
+                  else torch.cuda.ExternalStream(int(stream), device=device))
+    return torch.cuda.stream(stream)
+
+
 def workspace_for(shape, device=None) -> torch.Tensor:
     n = kvp_workspace_bytes(shape)
     if n == 0:
@@ -396,13 +410,6 @@ def evict_layer(q_win, k, v, window: int, budget: int, buffers: LayerBuffers | N
 # ---- the paged cache
 
 
-def _kept_for(stream, workspace):
-    """A workspace that the call made itself lives until `stream` is done with it."""
-    if stream is not None:
-        workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                else torch.cuda.ExternalStream(int(stream), device=workspace.device))
-
-
 def _device_of(t):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("a paged cache's tensors must be CUDA tensors")
@@ -447,12 +454,10 @@ def kvp_cache_append(shape, k_new, v_new, k_pages, v_pages, table, lens, lens_ou
 def kvp_cache_attend(shape, q, k_pages, v_pages, table, lens, out, lse=None, acc=None, workspace=None,
                      stream=None):
     """Attention of one token q [b, hq, d] over the cache; acc gains each row's weights."""
-    own = workspace is None
-    if own:
-        workspace = attend_workspace_for(shape, acc is not None, _device_of(q))
+    if workspace is None:
+        with _current(stream, _device_of(q)):
+            workspace = attend_workspace_for(shape, acc is not None, q.device)
     st = _kvp_binding.attend(shape, q, k_pages, v_pages, table, lens, out, lse, acc, workspace, stream)
-    if own:
-        _kept_for(stream, workspace)
     if st != KVP_OK:
         raise KvpError(st, "kvp_cache_attend")
 
@@ -463,13 +468,11 @@ def kvp_cache_evict(shape, evict, k_pages, v_pages, acc, acc_out, table, lens, l
     its budget (a KvpEvict, or a dict of make_evict's arguments). In place; acc_out may be acc
     and lens_out lens."""
     ev = make_evict(**evict) if isinstance(evict, dict) else _structure(evict, KvpEvict)
-    own = workspace is None
-    if own:
-        workspace = evict_workspace_for(shape, ev, _device_of(k_pages))
+    if workspace is None:
+        with _current(stream, _device_of(k_pages)):
+            workspace = evict_workspace_for(shape, ev, k_pages.device)
     st = _kvp_binding.evict(shape, ev, k_pages, v_pages, acc, acc_out, table, lens, lens_out, src, budgets,
                             workspace, stream)
-    if own:
-        _kept_for(stream, workspace)
     if st != KVP_OK:
         raise KvpError(st, "kvp_cache_evict")
 
