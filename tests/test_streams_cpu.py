@@ -61,3 +61,31 @@ def test_paged_cache_scratch(m, current, monkeypatch, stream, want):
     m.kvp_cache_evict(sh, m.make_evict(8), t, t, t, t, t, t, t, stream=stream)
     assert calls == [("attend", stream), ("evict", stream)]
     assert current.at_empty == [want, want]
+
+
+class Library:
+    """The C library, whose launching calls succeed without launching anything."""
+
+    def __init__(self, lib):
+        self.lib = lib
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes"):
+            return getattr(self.lib, name)
+        return lambda *a: 0
+
+
+@pytest.mark.parametrize("stream,want", [(None, "current"), (HANDLE, f"stream {HANDLE}")])
+def test_prefill_scratch_and_outputs(m, current, monkeypatch, stream, want):
+    monkeypatch.setattr(m, "_lib", Library(m._lib))
+    monkeypatch.setattr(m, "_ptr", lambda *a, **k: 16)
+    sh = m.make_shape(1, 4, 2, 64, 128, 16, 32)
+    q, k = torch.zeros(1, 4, 16, 64), torch.zeros(1, 2, 128, 64)
+    m.kvp_score(sh, q, k, k, k, stream=stream)
+    m.kvp_select(sh, k, k, stream=stream)
+    m.kvp_leverage(sh, k, k, torch.zeros(64, 8), k, stream=stream)
+    m.kvp_select_adaptive(sh, 0.2, k, k, k, stream=stream)
+    assert current.at_empty == [want] * 4
+    # evict_layer's outputs and workspace: at least these
+    m.evict_layer(q, k, k, 16, 32, stream=stream)
+    assert len(current.at_empty) > 7 and set(current.at_empty) == {want}

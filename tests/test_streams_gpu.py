@@ -59,3 +59,30 @@ def test_evict(given, rows, budget):
         got.append([bits(t) for t in (k, v, acc, lens)])
     for x, y in zip(*got):
         assert np.array_equal(x, y)
+
+
+@pytest.mark.parametrize("given", STREAMS)
+def test_prefill(given):
+    """Score, select and compact by evict_layer, and the leverage scores."""
+    m = kvp()
+    b, hq, hkv, d, L, w, B = 1, 8, 2, 64, 1500, 16, 200
+    g = torch.Generator().manual_seed(3)
+    q, k, v, r = (torch.randn(s, generator=g).to(torch.bfloat16).cuda()
+                  for s in ((b, hq, w, d), (b, hkv, L, d), (b, hkv, L, d), (d, 16)))
+    sh = m.make_shape(b, hq, hkv, d, L, w, B)
+    side, n = torch.cuda.Stream(), m.kvp_workspace_bytes(sh)
+    got = []
+    for stream in (None, STREAMS[given](side)):
+        lev = torch.empty((b, hkv, L), device="cuda")
+        torch.cuda.synchronize()
+        for call in ("layer", "leverage"):
+            if stream is not None:
+                busy(n)
+            if call == "layer":
+                buf = m.evict_layer(q, k, v, w, B, stream=stream)
+            else:
+                m.kvp_leverage(sh, k, v, r, lev, stream=stream)
+        torch.cuda.synchronize()
+        got.append([bits(t) for t in (buf.score, buf.idx, buf.k_out, buf.v_out, lev)])
+    for x, y in zip(*got):
+        assert np.array_equal(x, y)

@@ -261,7 +261,8 @@ def kvp_score(shape, q_win, k, v, score, s1=None, s2=None, workspace=None, strea
             _ptr(s1, "s1", torch.float32, (b, hkv, L), optional=True),
             _ptr(s2, "s2", torch.float32, (b, hkv, L), optional=True))
     if workspace is None:
-        workspace = workspace_for(sh, k.device)
+        with _current(stream, k.device):
+            workspace = workspace_for(sh, k.device)
     st = _lib.kvp_score(ctypes.byref(sh), *args, workspace.data_ptr(), workspace.numel(),
                         _stream(stream))
     if st != KVP_OK:
@@ -282,7 +283,8 @@ def kvp_select(shape, score, idx, workspace=None, stream=None):
     ps = _ptr(score, "score", torch.float32, (b, hkv, L))
     pi = _ptr(idx, "idx", torch.int32, (b, hkv, B))
     if workspace is None:
-        workspace = workspace_for(sh, score.device)
+        with _current(stream, score.device):
+            workspace = workspace_for(sh, score.device)
     st = _lib.kvp_select(ctypes.byref(sh), ps, pi, workspace.data_ptr(), workspace.numel(),
                          _stream(stream))
     if st != KVP_OK:
@@ -315,7 +317,8 @@ def kvp_leverage(shape, k, v, g, score, workspace=None, stream=None):
             _ptr(g, "g", torch.bfloat16, tuple(g.shape)))
     ps = _ptr(score, "score", torch.float32, (b, hkv, L))
     if workspace is None:
-        workspace = workspace_for(sh, k.device)
+        with _current(stream, k.device):
+            workspace = workspace_for(sh, k.device)
     st = _lib.kvp_leverage(ctypes.byref(sh), *args, int(g.shape[1]), ps, workspace.data_ptr(),
                            workspace.numel(), _stream(stream))
     if st != KVP_OK:
@@ -338,7 +341,8 @@ def kvp_select_adaptive(shape, alpha, score, idx, counts, workspace=None, stream
     pi = _ptr(idx, "idx", torch.int32, (b, hkv * B))
     pc = _ptr(counts, "counts", torch.int32, (b, hkv))
     if workspace is None:
-        workspace = adaptive_workspace_for(sh, score.device)
+        with _current(stream, score.device):
+            workspace = adaptive_workspace_for(sh, score.device)
     st = _lib.kvp_select_adaptive(ctypes.byref(sh), float(alpha), ps, pi, pc, workspace.data_ptr(),
                                   workspace.numel(), _stream(stream))
     if st != KVP_OK:
@@ -392,7 +396,8 @@ def evict_layer(q_win, k, v, window: int, budget: int, buffers: LayerBuffers | N
                 stream=None):
     """Score, select and compact one layer; returns the LayerBuffers holding the results.
 
-    q_win [b, hq, w, d], k and v [b, hkv, L, d]: bf16 CUDA tensors.
+    q_win [b, hq, w, d], k and v [b, hkv, L, d]: bf16 CUDA tensors. Buffers that are not given are
+    allocated on `stream`: they are that stream's memory, as if it had been the current one.
     """
     b, hq, w, d = q_win.shape
     _, hkv, L, _ = k.shape
@@ -400,7 +405,8 @@ def evict_layer(q_win, k, v, window: int, budget: int, buffers: LayerBuffers | N
         raise ValueError("q_win must hold exactly `window` queries per head")
     sh = make_shape(b, hq, hkv, d, L, window, budget)
     if buffers is None:
-        buffers = LayerBuffers(sh, k.device)
+        with _current(stream, k.device):
+            buffers = LayerBuffers(sh, k.device)
     kvp_score(sh, q_win, k, v, buffers.score, buffers.s1, buffers.s2, buffers.workspace, stream)
     kvp_select(sh, buffers.score, buffers.idx, buffers.workspace, stream)
     kvp_compact(sh, k, v, buffers.idx, buffers.k_out, buffers.v_out, stream)
