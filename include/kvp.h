@@ -336,8 +336,10 @@ typedef struct {
  *            at and past lens_out), to carry along what else a program keeps per row
  *   workspace  at least kvp_cache_evict_workspace_bytes(shape, evict) bytes (0 for a bad shape or
  *           policy)
- * A row that moves from or to a place without a page is not copied. Pages past
- * ceil(lens_out / P) hold no rows any more and may be given to others.
+ * A row that moves from or to a place without a page is not copied. A row without a page weighs
+ * zero and the lower of equal rows stay, so of those only the window's can move: their places keep
+ * the key and value that they had, and acc_out there is not written (give acc itself, or an acc_out
+ * that holds numbers). Pages past ceil(lens_out / P) hold no rows any more and may be given to others.
  */
 KVP_API size_t kvp_cache_evict_workspace_bytes(const kvp_cache_shape* shape, const kvp_evict* evict);
 KVP_API kvp_status kvp_cache_evict(const kvp_cache_shape* shape, const kvp_evict* evict,
