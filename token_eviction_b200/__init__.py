@@ -29,8 +29,8 @@ plus ``evict_layer``, which allocates the outputs and runs the first three calls
 ``LayerCache``, the paged cache that a decode reads: it takes what ``evict_layer`` kept, appends
 and attends token by token, and keeps to a budget.
 
-There is no fallback: if ``libkvp.so`` or ``_kvp_binding.so`` is missing or cannot be loaded,
-importing this package raises.
+There is no fallback: if ``libkvp.so`` is missing or cannot be loaded, importing this package
+raises; without ``_kvp_binding.so`` (or with a library that lacks them) the paged cache's calls do.
 """
 from __future__ import annotations
 
@@ -145,30 +145,51 @@ def _load():
     lib.kvp_workspace_status.restype = ctypes.c_int
     lib.kvp_score_static.argtypes = [S, P, P, P, P, P, P, P]
     lib.kvp_score_static.restype = ctypes.c_int
-    C, E = ctypes.POINTER(KvpCacheShape), ctypes.POINTER(KvpEvict)
-    lib.kvp_cache_append.argtypes = [C, P, P, ctypes.c_int32, P, P, P, P, P, P, P, P, P]
-    lib.kvp_cache_append.restype = ctypes.c_int
-    lib.kvp_cache_attend_workspace_bytes.argtypes = [C, ctypes.c_int32]
-    lib.kvp_cache_attend_workspace_bytes.restype = ctypes.c_size_t
-    lib.kvp_cache_attend.argtypes = [C, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
-    lib.kvp_cache_attend.restype = ctypes.c_int
-    lib.kvp_cache_evict_workspace_bytes.argtypes = [C, E]
-    lib.kvp_cache_evict_workspace_bytes.restype = ctypes.c_size_t
-    lib.kvp_cache_evict.argtypes = [C, E, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
-    lib.kvp_cache_evict.restype = ctypes.c_int
     lib.kvp_score_static_status.argtypes = [P]
     lib.kvp_score_static_status.restype = ctypes.c_int
     return lib
 
 
+class _Missing:
+    """Stands for a part that cannot be loaded: whoever uses it is told why."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the paged cache's calls: {self._why}: build it with "
+                          "`python token_eviction_b200/build.py` (there is no fallback implementation)")
+
+
+def _load_cache(lib):
+    """The library as the paged cache's calls use it, and their entry. Where either is missing (a library
+    from before them, a binding built for another torch), prefill eviction works without."""
+    P = ctypes.c_void_p
+    C, E = ctypes.POINTER(KvpCacheShape), ctypes.POINTER(KvpEvict)
+    try:
+        lib.kvp_cache_append.argtypes = [C, P, P, ctypes.c_int32, P, P, P, P, P, P, P, P, P]
+        lib.kvp_cache_append.restype = ctypes.c_int
+        lib.kvp_cache_attend_workspace_bytes.argtypes = [C, ctypes.c_int32]
+        lib.kvp_cache_attend_workspace_bytes.restype = ctypes.c_size_t
+        lib.kvp_cache_attend.argtypes = [C, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        lib.kvp_cache_attend.restype = ctypes.c_int
+        lib.kvp_cache_evict_workspace_bytes.argtypes = [C, E]
+        lib.kvp_cache_evict_workspace_bytes.restype = ctypes.c_size_t
+        lib.kvp_cache_evict.argtypes = [C, E, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        lib.kvp_cache_evict.restype = ctypes.c_int
+    except AttributeError as e:
+        missing = _Missing(f"{LIB_PATH} does not have them ({e})")
+        return missing, missing
+    try:
+        from . import _kvp_binding as binding
+    except ImportError as e:
+        return lib, _Missing(f"_kvp_binding.so cannot be loaded ({e})")
+    binding.use(*(ctypes.cast(f, P).value for f in (lib.kvp_cache_append, lib.kvp_cache_attend, lib.kvp_cache_evict)))
+    return lib, binding
+
+
 _lib = _load()
-try:
-    from . import _kvp_binding
-except ImportError as e:
-    raise ImportError(f"_kvp_binding.so cannot be loaded ({e}): build it with "
-                      "`python token_eviction_b200/build.py` (there is no fallback implementation)") from e
-_kvp_binding.use(*(ctypes.cast(f, ctypes.c_void_p).value
-                   for f in (_lib.kvp_cache_append, _lib.kvp_cache_attend, _lib.kvp_cache_evict)))
+_cache_lib, _kvp_binding = _load_cache(_lib)
 
 # Kernel launches one layer's kvp_score + kvp_select + kvp_compact makes: the fused
 # scoring kernel (both passes over K), the selection and the gather. kvp_score also
@@ -436,13 +457,13 @@ def _structure(x, kind):
 
 def attend_workspace_for(shape, accumulate=False, device=None) -> torch.Tensor:
     _structure(shape, KvpCacheShape)
-    n = int(_lib.kvp_cache_attend_workspace_bytes(ctypes.byref(shape), int(bool(accumulate))))
+    n = int(_cache_lib.kvp_cache_attend_workspace_bytes(ctypes.byref(shape), int(bool(accumulate))))
     return _cache_workspace(n, "kvp_cache_attend_workspace_bytes", device)
 
 
 def evict_workspace_for(shape, evict, device=None) -> torch.Tensor:
     _structure(shape, KvpCacheShape), _structure(evict, KvpEvict)
-    n = int(_lib.kvp_cache_evict_workspace_bytes(ctypes.byref(shape), ctypes.byref(evict)))
+    n = int(_cache_lib.kvp_cache_evict_workspace_bytes(ctypes.byref(shape), ctypes.byref(evict)))
     return _cache_workspace(n, "kvp_cache_evict_workspace_bytes", device)
 
 
