@@ -1,9 +1,12 @@
 """What the package needs to be imported: prefill eviction takes libkvp.so alone, of any age; the paged
-cache's calls say what they miss when they are called."""
+cache's calls say what they miss when they are called. And when its binding is built again."""
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+
+import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PKG = os.path.join(ROOT, "token_eviction_b200")
@@ -60,3 +63,33 @@ def test_a_missing_library_is_still_refused_at_import(tmp_path):
                          env={**os.environ, "KVP_LIBRARY": str(tmp_path / "none.so")})
     assert got.returncode != 0 and "no fallback" in got.stderr
 
+
+@pytest.fixture
+def builder(tmp_path, monkeypatch):
+    spec = importlib.util.spec_from_file_location("kvp_build_for_test", os.path.join(PKG, "build.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    monkeypatch.setattr(mod, "BINDING", str(tmp_path / "_kvp_binding.so"))
+    monkeypatch.setattr(mod, "ROOT", str(tmp_path))
+    made = []
+
+    def compile(cmd):
+        made.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    monkeypatch.setattr(mod.subprocess, "check_call", compile)
+    mod.made = made
+    return mod
+
+
+def test_the_binding_is_built_again_for_another_torch(builder, monkeypatch):
+    import torch
+    builder.build_binding()
+    builder.build_binding()
+    assert len(builder.made) == 1
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    builder.build_binding()
+    builder.build_binding()
+    assert len(builder.made) == 2
+    builder.build_binding(force=True)
+    assert len(builder.made) == 3

@@ -110,14 +110,18 @@ BINDING = os.path.join(PKG, "_kvp_binding.so")
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
-    src = os.path.join(CSRC, "kvp_binding.cpp")
-    deps = [src, os.path.join(INCLUDE, "kvp.h")]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in deps):
-        return BINDING
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension
+    src = os.path.join(CSRC, "kvp_binding.cpp")
+    deps = [src, os.path.join(INCLUDE, "kvp.h")]
+    # it holds to one torch and one Python: what it was built for is noted beside the objects
+    built_for = " ".join((torch.__version__, os.path.dirname(torch.__file__), sysconfig.get_config_var("SOABI") or ""))
+    note = os.path.join(ROOT, "_build", "binding.txt")
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in deps):
+        if os.path.exists(note) and open(note).read() == built_for:
+            return BINDING
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cuda = os.path.dirname(os.path.dirname(NVCC))
     tmp = BINDING + f".tmp{os.getpid()}"
@@ -130,6 +134,9 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(note), exist_ok=True)
+    with open(note, "w") as f:
+        f.write(built_for)
     return BINDING
 
 
