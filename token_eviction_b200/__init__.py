@@ -511,15 +511,20 @@ class LayerCache:
     Holds up to `capacity` rows per KV head, in pages of its own (table and pools may be replaced by
     a program that shares a pool between layers or requests); rows past them are dropped. `evict`: a
     KvpEvict; heads over its budget are cut back in every step, so capacity must exceed the budget.
+    `budgets` [batch, hkv] int32: each head's own budget, up to evict's (the counts of
+    kvp_select_adaptive, say, whose rows append(counts=) takes: without it every head that was
+    given more rows than evict's budget is cut back to that, and the others grow up to it).
     """
 
     def __init__(self, batch, hq, hkv, head_dim, capacity, page_size=64, evict: KvpEvict | None = None,
-                 dtype=torch.bfloat16, device="cuda"):
+                 dtype=torch.bfloat16, device="cuda", budgets=None):
         width = -(-capacity // page_size)
+        if evict is None and budgets is not None:
+            raise ValueError("budgets per head need an eviction policy: evict=make_evict(...)")
         if evict is not None and width * page_size <= evict.budget:
             raise ValueError("capacity must exceed the eviction's budget: a step appends before it evicts")
         self.shape = make_cache_shape(batch, hq, hkv, head_dim, page_size, batch * hkv * width, width, dtype)
-        self.evict_policy = evict
+        self.evict_policy, self.budgets = evict, budgets
         new = lambda shape, dt: torch.zeros(shape, dtype=dt, device=device)
         self.k_pages = new((self.shape.num_pages, page_size, head_dim), dtype)
         self.v_pages = torch.zeros_like(self.k_pages)
@@ -545,7 +550,7 @@ class LayerCache:
     def evict(self, stream=None):
         """Cuts every head that is over the budget back to it."""
         kvp_cache_evict(self.shape, self.evict_policy, self.k_pages, self.v_pages, self.acc, self.acc,
-                        self.table, self.lens, self.lens, None, None, self.evict_workspace, stream)
+                        self.table, self.lens, self.lens, None, self.budgets, self.evict_workspace, stream)
 
     def step(self, q, k_new, v_new, stream=None) -> torch.Tensor:
         """One decoded token: its key and value [b, hkv, 1, d] join the cache, q attends, and the cache is
