@@ -27,3 +27,8 @@ def test_budgets_per_head_reach_the_eviction(m, monkeypatch):
 def test_budgets_without_a_policy_are_refused(m):
     with pytest.raises(ValueError, match="polic"):
         m.LayerCache(1, 4, 2, 64, 64, 16, device="cpu", budgets=torch.tensor([[20, 12]], dtype=torch.int32))
+
+
+def test_evicting_without_a_policy_is_refused(m):
+    with pytest.raises(ValueError, match="without an eviction policy"):
+        m.LayerCache(1, 4, 2, 64, 64, 16, device="cpu").evict()

@@ -549,6 +549,8 @@ class LayerCache:
 
     def evict(self, stream=None):
         """Cuts every head that is over the budget back to it."""
+        if self.evict_policy is None:
+            raise ValueError("this cache was made without an eviction policy: evict=make_evict(...)")
         kvp_cache_evict(self.shape, self.evict_policy, self.k_pages, self.v_pages, self.acc, self.acc,
                         self.table, self.lens, self.lens, None, self.budgets, self.evict_workspace, stream)
 
