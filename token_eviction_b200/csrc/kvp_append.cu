@@ -108,10 +108,9 @@ __global__ void __launch_bounds__(kThreads) append_rows(const AppendArgs a) {
         int head, i;
         place_of(a, lane < here ? base + lane : -1, head, i);
         long long dst = -1;
-        if (head >= 0) {
+        if (head >= 0 && KVP_CHECK(head < a.c.heads && i >= 0, 501, head, i)) {
             const long long j = (long long)a.c.len(head) + i;
             if (j < a.c.cap()) dst = a.c.row(head, (int)j);
-            if (!KVP_CHECK(dst < ((long long)a.c.num_pages << a.c.page_shift), 501, (int)base, lane)) dst = -1;
             if (dst >= 0 && a.acc) a.acc[dst] = a.weight ? a.weight[base + lane] : 0.f;
         }
 #pragma unroll

@@ -216,11 +216,11 @@ template <int kStride>
 __device__ __forceinline__ void add_weights(const AttendArgs& a, int head, int j0, int j1, int tid, const float* lse2) {
     const int cap = a.c.cap();
     for (int j = j0 + tid * 4; j < j1; j += kStride * 4) {
+        if (!KVP_CHECK(head >= 0 && head < a.c.heads && j >= 0 && j + 3 < cap, 601, head, j)) continue;
         const long long row = a.c.row(head, j);              // four rows lie in one page
         if (row < 0) continue;
         const float* lp = a.logits + (size_t)head * a.G * cap + j;
         float* ap = a.acc + row;
-        if (!KVP_CHECK(row + 3 < ((long long)a.c.num_pages << a.c.page_shift), 601, head, j)) continue;
         float4 x = *(const float4*)ap;                       // (the page's next rows past the last one)
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll 4
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
         page_base = w.tile;
         const int row0 = (page_base + lane) * kTile + warp * kGroup;
         pages = -1;
-        if (row0 < w.len) {
+        if (row0 < w.len && KVP_CHECK(w.head >= 0 && w.head < a.c.heads && row0 >= 0, 603, w.head, row0)) {
             const int p = a.c.table[(size_t)w.head * a.c.max_pages + (row0 >> a.c.page_shift)];
             if (p < a.c.num_pages) pages = p;
         }
@@ -712,7 +712,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
         }
         if (valid > 0) {
             run.take(my_ring + stage * kStage, valid, a.scale2, [&](int r, int row, float x, float y) {
-                if (a.logits && gid + 8 * r < nq) *(float2*)(lp + r * 8 * lp_row + m.row0 + row) = make_float2(x, y);
+                if (a.logits && gid + 8 * r < nq && KVP_CHECK(m.row0 + row + 1 < a.c.cap(), 604, head, m.row0 + row))
+                    *(float2*)(lp + r * 8 * lp_row + m.row0 + row) = make_float2(x, y);
             });
         }
         if (m.valid_flags & kLast) {
@@ -733,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
                 if (whole) {
                     const float lse2 = put_output<T, D>(a, (size_t)head * a.G + g0 + row, val, st);
                     if (lane == 0) sh_lse2[row] = lse2;
-                } else {
+                } else if (KVP_CHECK(slot < 2 * kMaxGrid && segment < 2, 605, slot, step)) {
                     float* to = a.parts + ((size_t)slot * a.gq + row) * D + lane * kCols;
 #pragma unroll
                     for (int c = 0; c < kCols; ++c) to[c] = val[c];
@@ -753,8 +754,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attend_split(const Atten
                 x.c0 = cutting.owner(first);
                 x.n = cutting.owner(first + tiles_of(x.len) - 1) - x.c0 + 1;
                 x.later = cutting.begin(x.c0) < first;
-                a.cuts[slot] = x;
-                if (a.firsts && tile == 0) a.firsts[x.unit] = x;
+                if (KVP_CHECK(x.c0 >= 0 && x.n > 0 && x.c0 + x.n <= cutting.ctas() && tile >= 0, 606, x.c0, x.n)) a.cuts[slot] = x;
+                if (a.firsts && tile == 0 && KVP_CHECK(x.unit < kFewUnits, 607, x.unit, tile)) a.firsts[x.unit] = x;
             }
             if (whole && a.firsts && tid == 0) a.firsts[head * a.ng + m.sub].unit = -1;
             if (whole && a.logits && !a.lse2)
@@ -843,7 +844,8 @@ __global__ void __launch_bounds__(kShortThreads, 1) attend_short(const AttendArg
         if (valid > 0) {
             float* to = logits + gid * S::kLogitRow + (warp + kShortWarps * i) * kGroup;
             run.take(my_ring + i % kStages * kStage, valid, a.scale2, [&](int r, int row, float x, float y) {
-                if (a.acc) *(float2*)(to + r * 8 * S::kLogitRow + row) = make_float2(x, y);
+                if (a.acc && KVP_CHECK(gid + 8 * r < kQ && (warp + kShortWarps * i) * kGroup + row + 1 < S::kLogitRow, 608, head, i))
+                    *(float2*)(to + r * 8 * S::kLogitRow + row) = make_float2(x, y);
             });
         }
         __syncwarp();                                           // the stage has been read
@@ -886,7 +888,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) attend_short(const AttendArg
     }
     ptx::cluster_arrive();                                      // this thread has read the others' shared memory
     __syncthreads();
-    if (acc_row >= 0 && KVP_CHECK(acc_row + 3 < ((long long)a.c.num_pages << a.c.page_shift), 602, head, j)) {
+    if (acc_row >= 0 && KVP_CHECK(tid * 4 + 3 < S::kLogitRow, 602, head, j)) {
         for (int g = 0; g < nq; ++g) {
             const float4 t = *(const float4*)(logits + g * S::kLogitRow + tid * 4);
             const float l = sh_lse2[g];
@@ -972,7 +974,8 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendArgs 
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 const int part = base + i * kJoinWarps + warp;
-                if (part < p.n) y[i] = ((const Piece*)(a.parts + (p.slot(part) * a.gq + row) * D))[lane];
+                if (part < p.n && KVP_CHECK(p.slot(part) < 2 * kMaxGrid, 609, p.c0, part))
+                    y[i] = ((const Piece*)(a.parts + (p.slot(part) * a.gq + row) * D))[lane];
             }
         };
         read(0);
@@ -1038,7 +1041,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attend_join_few(const AttendA
             const int part = base + x * kJoinWarps;
             st[x] = make_float2(kLowest, 0.f);
             y[x] = Piece{};
-            if (part >= last) continue;
+            if (part >= last || !KVP_CHECK(p.slot(part) < 2 * kMaxGrid, 610, p.c0, part)) continue;
             const size_t at = p.slot(part) * a.gq + row;
             st[x] = a.stats[at];
             y[x] = ((const Piece*)(a.parts + at * D))[lane];
@@ -1100,7 +1103,6 @@ __global__ void __launch_bounds__(kJoinThreads) attend_weigh(const AttendArgs a,
     for (int j = blockIdx.x % per * kJoinThreads + threadIdx.x; j < len; j += per * kJoinThreads) {
         const long long row = a.c.row(head, j);
         if (row < 0) continue;
-        if (!KVP_CHECK(row < ((long long)a.c.num_pages << a.c.page_shift), 603, head, j)) continue;
         const float* lp = a.logits + (size_t)head * a.G * cap + j;
         const float drawn = a.acc[row];
         float sum = 0.f;

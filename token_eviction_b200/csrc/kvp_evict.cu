@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) evict_select_long(const EvictA
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             const size_t row = ((size_t)max(page, 0) << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
             if (there) x = *(const float4*)(a.acc + row);
-            if (in_smem && full)
+            if (in_smem && full && KVP_CHECK(j - lo + 4 <= a.slice, 709, head, j))
                 *(uint4*)(keys + (j - lo)) = make_uint4(key_of(x.x), key_of(x.y), key_of(x.z), key_of(x.w));
             if (there && copy) {
                 if (j + 4 <= stay) {
@@ -325,10 +325,12 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, int head, int firs
         float weight = 0.f;
         if (lane < here) {
             const int2 p = pair(base + lane);
-            from = a.c.row(head, p.x);
-            to = a.c.row(head, p.y);
-            if (a.src) a.src[(size_t)head * a.B + p.y] = p.x;
-            if (from < 0 || !KVP_CHECK(to < ((long long)a.c.num_pages << a.c.page_shift), 703, head, p.y)) to = -1;
+            if (KVP_CHECK(p.x >= 0 && p.x < a.c.cap() && p.y >= 0 && p.y < min(a.B, a.c.cap()), 703, p.x, p.y)) {
+                from = a.c.row(head, p.x);
+                to = a.c.row(head, p.y);
+                if (a.src) a.src[(size_t)head * a.B + p.y] = p.x;
+            }
+            if (from < 0) to = -1;
             if (to >= 0) weight = a.acc[from];
         }
         if (!kBarrier && to >= 0) a.acc_out[to] = weight;
@@ -617,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
                 const uint32_t other = __shfl_sync(0xffffffffu, mine, x);
                 place += (lows >> x & 1) && other < mine;
             }
-            if (is_low) {
+            if (is_low && KVP_CHECK(place < kFew, 705, head, place)) {
                 sh.to[place] = (int)mine;
                 sh.to_row[place] = a.c.row(head, (int)mine);
             }
@@ -751,11 +753,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
         if (own) {
             for (; out_low; out_low &= out_low - 1, ++at) {
                 const int j = j0 + __ffs(out_low) - 1;
+                if (!KVP_CHECK(at >= 0 && at < (here ? kFew : kOwn), 706, head, at)) break;
                 sh.to[at] = j;
                 if (here) sh.to_row[at] = a.c.row(head, j);
             }
             at = kept_high;
-            for (; in_high; in_high &= in_high - 1, ++at) sh.from[at] = j0 + __ffs(in_high) - 1;
+            for (; in_high; in_high &= in_high - 1, ++at)
+                if (KVP_CHECK(at >= 0 && at < kOwn, 707, head, at)) sh.from[at] = j0 + __ffs(in_high) - 1;
         } else {
             list_rows<kPer>(out_low, at, j0, [&](int i, int j) { if (KVP_CHECK(i >= 0 && i < a.B, 701, head, i)) to[i] = j; });
             list_rows<kPer>(in_high, kept_high, j0, [&](int i, int j) { if (KVP_CHECK(i >= 0 && i < a.B, 702, head, i)) from[i] = j; });
@@ -763,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
         if (!fill) {
             // evict_move fills in src and acc_out of the rows that stay: a bit each
             const uint32_t stays = low & (kept | first_bits(s));
-            if (j0 < split) {
+            if (j0 < split && KVP_CHECK((size_t)j0 / 8 + kPer / 8 <= a.stays_stride, 708, head, j0)) {
                 if (kPer == 16) ((uint16_t*)a.stays)[((size_t)head * a.stays_stride + j0 / 8) / 2] = (uint16_t)stays;
                 else a.stays[(size_t)head * a.stays_stride + j0 / 8] = (uint8_t)stays;
             }
@@ -783,10 +787,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) evict_select(const EvictArgs 
             const bool is_listed = i < listed;
             const int r = is_listed ? sh.from[i] - split : n - w - split + i - listed;     // source
             const int place = is_listed ? sh.to[i] : split + i - listed;
+            if (!KVP_CHECK(r >= 0 && r < kFew && listed <= kFew && place >= 0 && place < t, 704, r, place)) continue;
             const long long to_row = is_listed ? sh.to_row[i] : sh.row[i - listed];
             if (src && lane == 0) src[place] = split + r;
             if (sh.row[r] < 0 || to_row < 0) continue;
-            if (!KVP_CHECK(to_row < ((long long)a.c.num_pages << a.c.page_shift), 704, head, place)) continue;
             if (lane < 2 * chunks) pool[to_row * chunks] = ((const uint4*)keys)[r * 2 * chunks + lane];
             if (lane == 0) a.acc_out[to_row] = sh.weight[r];
         }
