@@ -508,9 +508,10 @@ class LayerCache:
     """One layer's paged cache through a decode: filled with the rows an eviction kept, then a token at
     a time appended, attended over and, where a budget is given, evicted by accumulated weight.
 
-    Holds up to `capacity` rows per KV head, in pages of its own (table and pools may be replaced by
-    a program that shares a pool between layers or requests); rows past them are dropped. `evict`: a
-    KvpEvict; heads over its budget are cut back in every step, so capacity must exceed the budget.
+    Holds up to `capacity` rows per KV head, rounded up to whole pages, in pages of its own (table, pools
+    and shape may be replaced by a program that shares a pool between layers or requests). Rows that no
+    longer fit are dropped and attention goes on without them: a head whose `lens` stands at
+    max_pages * page_size is full. `evict`: a KvpEvict; heads over its budget are cut back in every step, so capacity must exceed the budget.
     `budgets` [batch, hkv] int32: each head's own budget, up to evict's (the counts of
     kvp_select_adaptive, say, whose rows append(counts=) takes: without it every head that was
     given more rows than evict's budget is cut back to that, and the others grow up to it).
